@@ -239,6 +239,72 @@ const char* latentmoe_status_string(lmoe_status s);
 lmoe_status latentmoe_update_bias(lmoe_handle* h, const int32_t* expert_counts, const float* bias_in, float eta,
                                   float* bias_out, double* maxvio_out, void* stream);
 
+/* ---- Products without a handle -------------------------------------------
+ * The expert products on their own, for callers that hold rows in expert order
+ * (latentmoe_ep_front's send_rows and counts, or their own): the pages' expert
+ * loop runs up_proj and down_proj this way ("Nemotron 3 Ultra 架构 QA", Q5.6),
+ * one weight matrix per expert over that expert's rows.
+ *
+ * Common to these calls:
+ *  - All pointers are device memory of the current device, 16-byte aligned
+ *    (counts and fp8 scale outputs 4-byte). Asynchronous on `stream`; no
+ *    workspace, nothing allocated after the first call, no synchronisation; can
+ *    be captured into a CUDA graph; safe from several threads and streams at
+ *    once. Deterministic: the same inputs give the same bits.
+ *  - counts [n_groups] int32 on the device: rows of each group. Group e's rows
+ *    follow group e - 1's. The sum may be less than n_rows: rows behind the last
+ *    group are read by nobody and keep what they held, or are written as zeros
+ *    with zero_tail != 0. Negative counts are taken as 0, and rows past n_rows
+ *    as absent.
+ *  - ldx, lddy, ...: row pitch in elements, at least the row's length, a multiple
+ *    of 8. Weights are contiguous [n_groups, N, K]. 1 <= n_groups <= 1024;
+ *    N a multiple of 8, K of 8 (fp8: 16), both at most 2^24, at most 2^38
+ *    elements per operand (else LMOE_ERR_UNSUPPORTED). n_rows = 0 is allowed.
+ *  - Outputs are bf16 (one rounding from fp32, nearest-even) or fp32. NaN and
+ *    infinities stay in the rows (for dw: in the group) that they belong to.
+ *  - An output must not overlap an input.
+ *  - A device wait that runs out of its bound is recorded process-wide and
+ *    returned as LMOE_ERR_TIMEOUT by the next of these calls. */
+
+/* y[r, n] = sum_k x[r, k] w[e(r), n, k]: x [n_rows, K] bf16, w [n_groups, N, K]
+ * bf16, y [n_rows, N]. */
+lmoe_status latentmoe_grouped_gemm(const void* x, long long ldx, const void* w, const int32_t* counts, int n_groups,
+                                   int n_rows, int N, int K, void* y, long long ldy, lmoe_dtype y_dtype, int zero_tail,
+                                   void* stream);
+/* Its gradients. dx[r, k] = sum_n dy[r, n] w[e(r), n, k]: dy [n_rows, N] bf16,
+ * dx [n_rows, K]. */
+lmoe_status latentmoe_grouped_gemm_dx(const void* dy, long long lddy, const void* w, const int32_t* counts, int n_groups,
+                                      int n_rows, int N, int K, void* dx, long long lddx, lmoe_dtype dx_dtype,
+                                      int zero_tail, void* stream);
+/* dw[e, n, k] = sum over group e's rows of dy[r, n] x[r, k]; dw [n_groups, N, K]
+ * contiguous, written in full: zeros for a group without rows. */
+lmoe_status latentmoe_grouped_gemm_dw(const void* dy, long long lddy, const void* x, long long ldx, const int32_t* counts,
+                                      int n_groups, int n_rows, int N, int K, void* dw, lmoe_dtype dw_dtype,
+                                      void* stream);
+
+/* 8-bit quantisation of n_mat matrices [R, K] (x_dtype bf16 or fp32, row pitch
+ * ldx, matrices R * ldx apart): e4m3 codes [n_mat, R, K] and one fp32 scale per
+ * block of block_rows x 128 elements, block_rows 1 (activations: scales [n_mat,
+ * R, ceil(K / 128)]) or 128 (weights: scales [n_mat, ceil(R / 128), ceil(K /
+ * 128)]). Recipe, every step an fp32 operation rounded to nearest even:
+ *   a = max(amax(block), 2^-100)   scale = a / 448
+ *   code = nearest e4m3 to x * (448 / a), saturating at 448
+ * The element's value is code * scale. A NaN makes its block NaN (codes and
+ * scale); an infinity makes its block's scale infinite. K a multiple of 16, ldx
+ * of 8 (fp32: 4), at most 2^31 - 1 row blocks. */
+lmoe_status latentmoe_quantize_fp8(const void* x, long long ldx, lmoe_dtype x_dtype, int n_mat, int R, int K,
+                                   int block_rows, void* codes, float* scales, void* stream);
+/* The product of quantised operands, with nb = ceil(K / 128):
+ *   y[r, n] = sum_b xs[r, b] ws[e(r), n / 128, b] sum_{k in block b} xq[r, k] wq[e(r), n, k]
+ * xq [n_rows, K] and wq [n_groups, N, K] e4m3, xs [n_rows, nb] and ws [n_groups,
+ * ceil(N / 128), nb] fp32, all contiguous. Products within a block are exact and
+ * summed in the tensor core's fp32; the two scales' product is rounded to fp32
+ * once and applied with one fused multiply-add per block. counts may be NULL
+ * with n_groups = 1: one matrix for all rows. */
+lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, const float* ws, const int32_t* counts,
+                               int n_groups, int n_rows, int N, int K, void* y, long long ldy, lmoe_dtype y_dtype,
+                               int zero_tail, void* stream);
+
 /* ---- diagnostics --------------------------------------------------------- */
 typedef enum {
     LMOE_OPT_GEMM_PATH = 0,      /* 0 auto, 1 tcgen05 prefill tiles (128 x BN per SM), 2 tcgen05

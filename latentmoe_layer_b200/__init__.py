@@ -33,7 +33,8 @@ EXPORTS = ["latentmoe_create", "latentmoe_workspace_size", "latentmoe_route", "l
            "latentmoe_destroy", "latentmoe_status_string", "latentmoe_set_option", "latentmoe_read_stats",
            "latentmoe_selftest_bounded_wait", "latentmoe_set_profile_events", "latentmoe_route_noalloc", "latentmoe_update_bias", "latentmoe_forward_block",
            "latentmoe_quantize_nvfp4", "latentmoe_ep_front", "latentmoe_ep_workspace_size", "latentmoe_ep_experts",
-           "latentmoe_ep_back", "latentmoe_workspace_layout"]
+           "latentmoe_ep_back", "latentmoe_workspace_layout", "latentmoe_grouped_gemm", "latentmoe_grouped_gemm_dx",
+           "latentmoe_grouped_gemm_dw", "latentmoe_quantize_fp8", "latentmoe_gemm_fp8"]
 
 
 class lmoe_config(ctypes.Structure):
@@ -102,12 +103,19 @@ def load():
     lib.latentmoe_ep_experts.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, sz, vp]
     lib.latentmoe_ep_back.argtypes = [vp, vp, i32, vp, vp, sz, vp]
     lib.latentmoe_workspace_layout.argtypes = [vp, i32, ctypes.POINTER(lmoe_ws_layout)]
+    ll = ctypes.c_longlong
+    lib.latentmoe_grouped_gemm.argtypes = [vp, ll, vp, vp, i32, i32, i32, i32, vp, ll, i32, i32, vp]
+    lib.latentmoe_grouped_gemm_dx.argtypes = [vp, ll, vp, vp, i32, i32, i32, i32, vp, ll, i32, i32, vp]
+    lib.latentmoe_grouped_gemm_dw.argtypes = [vp, ll, vp, ll, vp, i32, i32, i32, i32, vp, i32, vp]
+    lib.latentmoe_quantize_fp8.argtypes = [vp, ll, i32, i32, i32, i32, i32, vp, vp, vp]
+    lib.latentmoe_gemm_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, ll, i32, i32, vp]
     for f in ("latentmoe_create", "latentmoe_workspace_size", "latentmoe_route", "latentmoe_forward",
               "latentmoe_set_option", "latentmoe_read_stats", "latentmoe_selftest_bounded_wait",
               "latentmoe_set_profile_events", "latentmoe_route_noalloc", "latentmoe_update_bias",
               "latentmoe_forward_block", "latentmoe_quantize_nvfp4", "latentmoe_ep_front",
               "latentmoe_ep_workspace_size", "latentmoe_ep_experts", "latentmoe_ep_back",
-              "latentmoe_workspace_layout"):
+              "latentmoe_workspace_layout", "latentmoe_grouped_gemm", "latentmoe_grouped_gemm_dx",
+              "latentmoe_grouped_gemm_dw", "latentmoe_quantize_fp8", "latentmoe_gemm_fp8"):
         getattr(lib, f).restype = i32
     _lib = lib
     return lib
@@ -202,6 +210,10 @@ def latentmoe_workspace_layout(h, T: int):
 
 def latentmoe_selftest_bounded_wait(h) -> int:
     return load().latentmoe_selftest_bounded_wait(h)
+
+
+# ---------------------------------------------------------------- products without a handle
+from .ops import gemm_fp8, grouped_gemm, grouped_gemm_dw, grouped_gemm_dx, quantize_fp8  # noqa: E402,F401
 
 
 # ---------------------------------------------------------------- convenience wrapper

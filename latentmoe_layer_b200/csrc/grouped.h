@@ -1,0 +1,37 @@
+// grouped.h -- parameters and launchers of the grouped products and of the
+// block-scaled 8-bit quantiser.
+#pragma once
+#include "lmoe_internal.h"
+
+namespace lmoe {
+
+enum GgOp : int { GG_FWD = 0, GG_DX = 1, GG_DW = 2, GG_FP8 = 3 };
+
+struct alignas(64) GgParams {
+    CUtensorMap a_map;    // feature-side operand
+    CUtensorMap b_map;    // row-side operand, boxes of 128 rows (GG_DW: 64 x 64)
+    CUtensorMap b_small;  // row-side operand, boxes of 16 rows (not GG_DW)
+    const int* counts;    // [n_groups] rows per group; null: one group of n_rows rows
+    const float* a_scale; // GG_FP8: [n_groups, ceil(feat / 128), ceil(cdim / 128)]
+    const float* b_scale; // GG_FP8: [n_rows, ceil(cdim / 128)]
+    const uint16_t* x;    // GG_DW: the operands again, for the partial k-blocks
+    const uint16_t* dy;
+    long long ldx, lddy;
+    void* out;
+    long long ldo;        // output row pitch, elements
+    int n_groups, n_rows;
+    int feat;             // output columns (the MMA's M side)
+    int cdim;             // contraction length (GG_DW: the group's rows instead)
+    int cols;             // GG_DW: rows of each dW[e]
+    int out_f32;
+    int zero_tail;        // 1: rows behind the last group are written as zeros
+    int chunk_kb;         // k-blocks per TMEM chunk (GG_FP8: always 1)
+    int* err;
+    unsigned spin;
+};
+
+cudaError_t launch_grouped(int op, const GgParams& P, cudaStream_t s);
+cudaError_t launch_quantize_fp8(const void* x, bool f32, long long ldx, int n_mat, int rows, int cols, int block_rows,
+                                uint8_t* codes, float* scales, cudaStream_t s);
+
+}  // namespace lmoe

@@ -1,0 +1,245 @@
+// ops.cu -- C entry points of the products that need no layer handle: grouped
+// products, their gradients, the 8-bit quantiser and the block-scaled 8-bit
+// product (include/latentmoe.h). Argument checks, TMA descriptors, one launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <string.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "grouped.h"
+
+using namespace lmoe;
+
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+constexpr unsigned kOpsSpin = 1u << 24;
+
+// What the entry points share, made once per process: the driver's descriptor
+// encoder and a pinned word that a kernel whose bounded wait ran out writes
+// (mapped into every device's address space).
+struct OpsState {
+    EncodeTiledFn encode = nullptr;
+    int* herr = nullptr;
+    int* derr = nullptr;
+};
+std::mutex g_ops_mu;
+OpsState g_ops;
+std::atomic<bool> g_ops_ready{false};
+
+lmoe_status ops_state(const OpsState** out) {
+    if (!g_ops_ready.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(g_ops_mu);
+        if (!g_ops_ready.load(std::memory_order_relaxed)) {
+            OpsState st;
+            // the first call may come while a stream is being captured: the allocation is not part of the graph
+            cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+            if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return LMOE_ERR_CUDA;
+            void* fn = nullptr;
+            cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+            bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+                      q == cudaDriverEntryPointSuccess && fn;
+            ok = ok && cudaHostAlloc(reinterpret_cast<void**>(&st.herr), 64, cudaHostAllocMapped | cudaHostAllocPortable) ==
+                           cudaSuccess;
+            ok = ok && cudaHostGetDevicePointer(reinterpret_cast<void**>(&st.derr), st.herr, 0) == cudaSuccess;
+            if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) ok = false;
+            if (!ok) {
+                if (st.herr) cudaFreeHost(st.herr);
+                return LMOE_ERR_CUDA;
+            }
+            *st.herr = 0;
+            st.encode = reinterpret_cast<EncodeTiledFn>(fn);
+            g_ops = st;
+            g_ops_ready.store(true, std::memory_order_release);
+        }
+    }
+    *out = &g_ops;
+    return LMOE_OK;
+}
+
+// An error that an earlier launch recorded is reported once, by the next call.
+lmoe_status take_error(const OpsState& st) {
+    const int v = __atomic_exchange_n(st.herr, 0, __ATOMIC_ACQ_REL);
+    return v ? static_cast<lmoe_status>(v) : LMOE_OK;
+}
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline lmoe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA; }
+
+// [mats, rows, cols] with a row pitch, boxes of 128 bytes x box_rows, 128-byte
+// swizzle; indices past the end are filled with zeros.
+bool encode(const OpsState& st, CUtensorMap* m, const void* base, bool bf16, long long mats, long long rows, long long cols,
+            long long pitch, int box_rows) {
+    const int esz = bf16 ? 2 : 1;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)mats};
+    cuuint64_t strides[2] = {(cuuint64_t)(pitch * esz), (cuuint64_t)(pitch * rows * esz)};
+    cuuint32_t box[3] = {(cuuint32_t)(128 / esz), (cuuint32_t)box_rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return st.encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                     const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr long long kMaxDim = 1LL << 24;        // N, K
+constexpr long long kMaxElems = 1LL << 38;      // elements of one operand
+constexpr long long kMaxTiles = 1LL << 30;      // tiles of one launch
+
+// Sizes of a product: n_rows rows in n_groups groups, weights [n_groups, N, K].
+lmoe_status check_sizes(int n_groups, int n_rows, int N, int K, int k_align) {
+    if (n_groups <= 0 || n_rows < 0 || N <= 0 || K <= 0) return LMOE_ERR_INVALID_ARG;
+    if (n_groups > kMaxE || N % 8 || K % k_align || N > kMaxDim || K > kMaxDim) return LMOE_ERR_UNSUPPORTED;
+    if ((long long)n_groups * N > kMaxElems / K) return LMOE_ERR_UNSUPPORTED;
+    const long long side = N > K ? N : K;
+    if (((long long)n_rows / 256 + n_groups + 1) * ((side + 255) / 256) > kMaxTiles ||
+        (long long)n_groups * ((N + 255) / 256) * ((K + 255) / 256) > kMaxTiles)
+        return LMOE_ERR_UNSUPPORTED;
+    return LMOE_OK;
+}
+// A row-major operand: 16-byte aligned base and rows, no overlapping rows. A
+// matrix without rows has no address to check.
+lmoe_status check_rows(const void* p, long long ld, int n_rows, int cols, int align_elems) {
+    if (n_rows == 0) return LMOE_OK;
+    if (!p || !aligned(p, 16) || ld < cols || ld % align_elems) return LMOE_ERR_INVALID_ARG;
+    if (ld > kMaxElems / n_rows) return LMOE_ERR_UNSUPPORTED;
+    return LMOE_OK;
+}
+lmoe_status check_counts(const int32_t* counts) {
+    return counts && aligned(counts, 4) ? LMOE_OK : LMOE_ERR_INVALID_ARG;
+}
+bool is_out_type(lmoe_dtype t) { return t == LMOE_BF16 || t == LMOE_FP32; }
+
+// Contraction accumulated in TMEM before it is added into fp32 registers, in
+// 64-deep k-blocks: 512 deep for fp32 outputs, all of it for bf16 outputs.
+int chunk_blocks(lmoe_dtype out) { return out == LMOE_FP32 ? 8 : 1 << 28; }
+
+GgParams base_params(const OpsState& st, const int32_t* counts, int n_groups, int n_rows, lmoe_dtype out_type) {
+    GgParams P;
+    memset(&P, 0, sizeof(P));
+    P.counts = counts;
+    P.n_groups = n_groups;
+    P.n_rows = n_rows;
+    P.out_f32 = out_type == LMOE_FP32;
+    P.chunk_kb = chunk_blocks(out_type);
+    P.err = st.derr;
+    P.spin = kOpsSpin;
+    return P;
+}
+
+// y [n_rows, N] = x W^T (dx = false) or dx [n_rows, K] = dy W (dx = true).
+lmoe_status run_rows(bool dx, const void* a, long long lda, const void* w, const int32_t* counts, int n_groups, int n_rows,
+                     int N, int K, void* out, long long ldo, lmoe_dtype out_type, int zero_tail, void* stream) {
+    lmoe_status s = check_sizes(n_groups, n_rows, N, K, 8);
+    if (s != LMOE_OK) return s;
+    const int in_cols = dx ? N : K, out_cols = dx ? K : N;
+    if (!is_out_type(out_type) || !w || !aligned(w, 16)) return LMOE_ERR_INVALID_ARG;
+    if ((s = check_counts(counts)) != LMOE_OK || (s = check_rows(a, lda, n_rows, in_cols, 8)) != LMOE_OK ||
+        (s = check_rows(out, ldo, n_rows, out_cols, 8)) != LMOE_OK)
+        return s;
+    if (n_rows == 0) return LMOE_OK;
+    const OpsState* st = nullptr;
+    if ((s = ops_state(&st)) != LMOE_OK || (s = take_error(*st)) != LMOE_OK) return s;
+    GgParams P = base_params(*st, counts, n_groups, n_rows, out_type);
+    P.out = out;
+    P.ldo = ldo;
+    P.feat = out_cols;
+    P.cdim = in_cols;
+    P.zero_tail = zero_tail != 0;
+    if (!encode(*st, &P.a_map, w, true, n_groups, N, K, K, dx ? 64 : 128) ||
+        !encode(*st, &P.b_map, a, true, 1, n_rows, in_cols, lda, 128) ||
+        !encode(*st, &P.b_small, a, true, 1, n_rows, in_cols, lda, 16))
+        return LMOE_ERR_CUDA;
+    return cuda_status(launch_grouped(dx ? GG_DX : GG_FWD, P, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+lmoe_status latentmoe_grouped_gemm(const void* x, long long ldx, const void* w, const int32_t* counts, int n_groups,
+                                   int n_rows, int N, int K, void* y, long long ldy, lmoe_dtype y_dtype, int zero_tail,
+                                   void* stream) {
+    return run_rows(false, x, ldx, w, counts, n_groups, n_rows, N, K, y, ldy, y_dtype, zero_tail, stream);
+}
+
+lmoe_status latentmoe_grouped_gemm_dx(const void* dy, long long lddy, const void* w, const int32_t* counts, int n_groups,
+                                      int n_rows, int N, int K, void* dx, long long lddx, lmoe_dtype dx_dtype,
+                                      int zero_tail, void* stream) {
+    return run_rows(true, dy, lddy, w, counts, n_groups, n_rows, N, K, dx, lddx, dx_dtype, zero_tail, stream);
+}
+
+lmoe_status latentmoe_grouped_gemm_dw(const void* dy, long long lddy, const void* x, long long ldx, const int32_t* counts,
+                                      int n_groups, int n_rows, int N, int K, void* dw, lmoe_dtype dw_dtype,
+                                      void* stream) {
+    lmoe_status s = check_sizes(n_groups, n_rows, N, K, 8);
+    if (s != LMOE_OK) return s;
+    if (!is_out_type(dw_dtype) || !dw || !aligned(dw, 16)) return LMOE_ERR_INVALID_ARG;
+    if ((s = check_counts(counts)) != LMOE_OK || (s = check_rows(dy, lddy, n_rows, N, 8)) != LMOE_OK ||
+        (s = check_rows(x, ldx, n_rows, K, 8)) != LMOE_OK)
+        return s;
+    const OpsState* st = nullptr;
+    if ((s = ops_state(&st)) != LMOE_OK || (s = take_error(*st)) != LMOE_OK) return s;
+    if (n_rows == 0)  // no rows anywhere: every gradient is zero
+        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)n_groups * N * K * (dw_dtype == LMOE_FP32 ? 4 : 2),
+                                           static_cast<cudaStream_t>(stream)));
+    GgParams P = base_params(*st, counts, n_groups, n_rows, dw_dtype);
+    P.x = static_cast<const uint16_t*>(x);
+    P.dy = static_cast<const uint16_t*>(dy);
+    P.ldx = ldx;
+    P.lddy = lddy;
+    P.out = dw;
+    P.ldo = K;
+    P.feat = K;
+    P.cols = N;
+    if (!encode(*st, &P.a_map, x, true, 1, n_rows, K, ldx, 64) || !encode(*st, &P.b_map, dy, true, 1, n_rows, N, lddy, 64))
+        return LMOE_ERR_CUDA;
+    return cuda_status(launch_grouped(GG_DW, P, static_cast<cudaStream_t>(stream)));
+}
+
+lmoe_status latentmoe_quantize_fp8(const void* x, long long ldx, lmoe_dtype x_dtype, int n_mat, int R, int K,
+                                   int block_rows, void* codes, float* scales, void* stream) {
+    if (n_mat < 0 || R < 0 || K <= 0 || !is_out_type(x_dtype) || (block_rows != 1 && block_rows != 128))
+        return LMOE_ERR_INVALID_ARG;
+    if (n_mat == 0 || R == 0) return LMOE_OK;
+    if (!x || !codes || !scales || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4) || ldx < K)
+        return LMOE_ERR_INVALID_ARG;
+    if (ldx % (x_dtype == LMOE_FP32 ? 4 : 8)) return LMOE_ERR_INVALID_ARG;
+    if (K % 16 || K > kMaxDim || n_mat > 65535 || (block_rows == 128 && R > 65535 * 128)) return LMOE_ERR_UNSUPPORTED;
+    const long long rows = (long long)n_mat * R;
+    if (ldx > kMaxElems / rows || rows * ((K + 127) / 128) > 0x7FFFFFFFLL) return LMOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_quantize_fp8(x, x_dtype == LMOE_FP32, ldx, n_mat, R, K, block_rows,
+                                           static_cast<uint8_t*>(codes), scales, static_cast<cudaStream_t>(stream)));
+}
+
+lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, const float* ws, const int32_t* counts,
+                               int n_groups, int n_rows, int N, int K, void* y, long long ldy, lmoe_dtype y_dtype,
+                               int zero_tail, void* stream) {
+    lmoe_status s = check_sizes(n_groups, n_rows, N, K, 16);
+    if (s != LMOE_OK) return s;
+    if (!is_out_type(y_dtype) || !wq || !aligned(wq, 16) || !ws || !aligned(ws, 16)) return LMOE_ERR_INVALID_ARG;
+    if (counts ? !aligned(counts, 4) : n_groups != 1) return LMOE_ERR_INVALID_ARG;
+    if (n_rows && (!xs || !aligned(xs, 16))) return LMOE_ERR_INVALID_ARG;
+    if ((s = check_rows(xq, K, n_rows, K, 16)) != LMOE_OK || (s = check_rows(y, ldy, n_rows, N, 8)) != LMOE_OK) return s;
+    if (n_rows == 0) return LMOE_OK;
+    const OpsState* st = nullptr;
+    if ((s = ops_state(&st)) != LMOE_OK || (s = take_error(*st)) != LMOE_OK) return s;
+    GgParams P = base_params(*st, counts, n_groups, n_rows, y_dtype);
+    P.a_scale = ws;
+    P.b_scale = xs;
+    P.out = y;
+    P.ldo = ldy;
+    P.feat = N;
+    P.cdim = K;
+    P.zero_tail = zero_tail != 0;
+    if (!encode(*st, &P.a_map, wq, false, n_groups, N, K, K, 128) ||
+        !encode(*st, &P.b_map, xq, false, 1, n_rows, K, K, 128) || !encode(*st, &P.b_small, xq, false, 1, n_rows, K, K, 16))
+        return LMOE_ERR_CUDA;
+    return cuda_status(launch_grouped(GG_FP8, P, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
