@@ -67,13 +67,14 @@ constexpr int kGgEpiWarps = 8;
 constexpr int kGgRaster = 8;          // N-side tiles per raster block (shared weight reads in L2)
 constexpr int kScaleBatch = 4;        // k-blocks per batch of scale products
 // registers per thread: 128 x kProdRegs + 256 x kEpiRegs must not exceed 384 x kLaunchRegs
-constexpr int kLaunchRegs = 168, kProdRegs = 56, kEpiRegs = 224;
+constexpr int kLaunchRegs = 168, kProdRegs = 72, kEpiRegs = 216;
 static_assert(128 * kProdRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "register split");
 
 struct alignas(1024) GgShared {
     uint8_t a[kGgStages][kGgABytes];
     uint8_t b[kGgStages][kGgBBytes];
     float scale[2][kScaleBatch][kGgBN];
+    uint8_t stage[kGgEpiWarps][2048];  // output rows on their way to 16-byte stores
     int off[kMaxE + 2];    // first row of each group, then the end of the last group, then n_rows
     int tiles[kMaxE + 2];  // tile prefix per group
     long long wsum[kGgThreads / 32];
@@ -177,6 +178,9 @@ __device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, i
     const int ms = min(kGgRaster, ct - g * kGgRaster);
     const int c = g * kGgRaster + r % ms;
     const int cnt = S.off[e + 1] - S.off[e];
+    // a group's rows are spread evenly over its tiles (in steps of 32): pairs take tiles in
+    // turn, so a full tile here and a short one there would leave some pairs waiting
+    const int per = OP == GG_DW ? kGgBN : (ceil_div(cnt, ct) + 31) & ~31;
     GgTile ti;
     ti.e = e;
     ti.feat0 = (r / ms) * 256;
@@ -187,9 +191,9 @@ __device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, i
         ti.nkb = ceil_div(cnt, 64);
         ti.rem = cnt & 63;
     } else {
-        ti.row0 = S.off[e] + c * kGgBN;
+        ti.row0 = S.off[e] + c * per;
         ti.col0 = 0;
-        ti.ncols = min(kGgBN, cnt - c * kGgBN);
+        ti.ncols = min(per, cnt - c * per);
         ti.nkb = e < P.n_groups ? ceil_div(P.cdim, OP == GG_FP8 ? 128 : 64) : 0;
         ti.rem = 0;
     }
@@ -205,6 +209,11 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
         "l"(reinterpret_cast<uint64_t>(map)), "r"(leader_bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+
+// GG_FP8: 128-deep blocks handed to the epilogue at once, side by side in a
+// 256-column buffer: a narrow tile's block is over too soon to pay for a hand-over
+// of its own. Divides kScaleBatch.
+__device__ __forceinline__ int blocks_per_drain(int neff) { return neff <= 64 ? 4 : neff <= 128 ? 2 : 1; }
 
 template <bool kF8>
 __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -231,6 +240,25 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
     d |= (uint64_t)1u << 46;
     d |= (uint64_t)2u << 61;
     return d;
+}
+
+// Arrive on another CTA's barrier without its release at cluster scope: that would
+// first wait for the thread's own stores to global memory (1.3K to 3.7K cycles per
+// hand-over of a TMEM buffer). Nothing this thread wrote is handed over here: its
+// TMEM loads have completed (tcgen05.wait::ld, tcgen05.fence).
+__device__ __forceinline__ void mbar_arrive_cluster_bare(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// One lane of a converged warp; the compiler then knows the branch is uniform.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // try_wait that acquires at cluster scope: the arrivals come from both CTAs.
@@ -273,26 +301,115 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // GG_DW: 64 threads copy the last, partial k-block of one operand: 64
 // contraction rows (rows row .. row + rem of src, zeros behind) x `width`
 // columns from column c0, zeros past column `limit`. Sub-tiles of 64 columns,
-// 128-byte rows, 16-byte pieces swizzled by the row's index modulo 8.
+// 128-byte rows, 16-byte pieces swizzled by the row's index modulo 8. The copies
+// are asynchronous, all of them in flight at once (registers would hold a few).
 __device__ __forceinline__ void copy_partial(uint8_t* dst, const uint16_t* src, long long ld, int row, int rem, int c0,
                                              int limit, int width, int tid) {
-    const int pieces = width / 8;  // 16-byte pieces per row, a multiple of 8
-    for (int i0 = tid; i0 < 64 * pieces; i0 += 64 * 4) {
-        uint4 v[4];
+    const uint32_t base = smem_u32(dst);
+    const int shift = width == 128 ? 4 : 3;  // 16-byte pieces per row: 16 or 8
+    for (int i = tid; i < 64 << shift; i += 64) {
+        const int r = i >> shift, q = i & ((1 << shift) - 1), c = c0 + q * 8;
+        const bool in = r < rem && c < limit;
+        const uint16_t* p = in ? src + (long long)(row + r) * ld + c : src;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         base + (uint32_t)((q >> 3) * 8192 + r * 128 + (((q & 7) ^ (r & 7)) << 4))),
+                     "l"(p), "r"(in ? 16 : 0)
+                     : "memory");
+    }
+}
+
+// 16 TMEM lanes x 32 columns: register 4 b + 2 s + j holds lane (l / 4) + 8 s, column
+// 8 b + 2 (l % 4) + j of thread l.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+// Waits for the loads so far; the registers pass through so that no use moves ahead of it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+// Four 8 x 8 matrices of 16-bit values, transposed on their way to shared memory.
+__device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+// The warp's accumulators: acc[h][b][s] holds features 16 h + 8 s + l / 4 of the
+// warp's 32, columns (output rows) 8 b + 2 (l % 4) and the next one.
+typedef uint64_t Acc[2][16][2];
+
+// Stores the warp's 32 features x nv output rows; `out` points at its first feature in
+// the first row, `feats` features exist from there. Transposed through 2 KB of
+// shared memory (bf16: 32 rows of 64 bytes by stmatrix; fp32: 16 rows of 128 bytes;
+// pieces swizzled so that neither side conflicts) into 16-byte stores of whole
+// sectors: two-byte stores straight from the registers took 10K cycles per tile.
+__device__ __forceinline__ void store_rows(const Acc& acc, uint8_t* stage, void* out, long long ldo, int nv, int feats,
+                                           bool f32, int lane) {
+    if (f32) {
+        float* st = reinterpret_cast<float*>(stage);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + 64 * u;
-            const int r = i / pieces, c = c0 + (i % pieces) * 8;
-            v[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rem && c < limit)
-                v[u] = __ldg(reinterpret_cast<const uint4*>(src + (long long)(row + r) * ld + c));
+        for (int rb = 0; rb < 8; ++rb) {
+            if (rb * 16 >= nv) break;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        float lo, hi;
+                        unpack2(acc[h][rb * 2 + b][s], lo, hi);
+                        float* p = st + (b * 8 + 2 * (lane & 3)) * 32 + ((h * 16 + s * 8 + (lane >> 2)) ^ ((lane & 3) << 3));
+                        p[0] = lo;
+                        p[32] = hi;
+                    }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (lane >> 3) + 4 * i, f = (lane & 7) * 4;
+                const float4 v = *reinterpret_cast<const float4*>(st + row * 32 + (f ^ (((row >> 1) & 3) << 3)));
+                if (rb * 16 + row < nv && f < feats)
+                    *reinterpret_cast<float4*>(static_cast<float*>(out) + (long long)(rb * 16 + row) * ldo + f) = v;
+            }
+            __syncwarp();
         }
+    } else {
+        const uint32_t st = smem_u32(stage);
+        const int m = lane >> 3, r8 = lane & 7;
+        const uint32_t dst = st + (uint32_t)(r8 * 64 + ((m ^ ((r8 >> 1) & 3)) << 4));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + 64 * u;
-            const int r = i / pieces, q = i % pieces;
-            if (r < 64)
-                *reinterpret_cast<uint4*>(dst + (q >> 3) * 8192 + r * 128 + (((q & 7) ^ (r & 7)) << 4)) = v[u];
+        for (int rb = 0; rb < 4; ++rb) {
+            if (rb * 32 >= nv) break;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    unpack2(acc[i >> 1][rb * 4 + b][i & 1], lo, hi);
+                    v[i] = pack_bf16x2(lo, hi);
+                }
+                stmatrix_trans(dst + b * 512, v[0], v[1], v[2], v[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (lane >> 2) + 8 * i, f = (lane & 3) * 8;
+                const uint4 v = ld_shared_v4(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+                if (rb * 32 + row < nv && f < feats)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (long long)(rb * 32 + row) * ldo + f) = v;
+            }
+            __syncwarp();
         }
     }
 }
@@ -323,8 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         mbar_init(&S.done, 1);
         fence_mbar_init();
         prefetch_tmap(&P.a_map);
-        prefetch_tmap(&P.b_map);
-        if (!kBMN) prefetch_tmap(&P.b_small);
+        for (int i = 0; i < (kBMN ? 1 : 4); ++i) prefetch_tmap(&P.b_map[i]);
     }
     if (warp == 1) {
         tmem_alloc_pair(&S.tmem, 512);
@@ -339,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProdRegs));
-        if (warp == 0 && lane == 0) {
+        if (warp == 0 && elect_one()) {
             // -------------------------------------------- TMA producer (both CTAs)
             int stage = 0, e = 0;
             uint32_t phase = 0, issued = 0, issued_par = 0;
@@ -371,17 +487,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                             const int r = ti.row0 + kb * 64;
                             tma_load_3d_pair(S.a[stage], &P.a_map, bar, f0, r, 0);
                             tma_load_3d_pair(S.a[stage] + 8192, &P.a_map, bar, f0 + 64, r, 0);
-                            tma_load_3d_pair(S.b[stage], &P.b_map, bar, b0, r, 0);
-                            if (half > 64) tma_load_3d_pair(S.b[stage] + 8192, &P.b_map, bar, b0 + 64, r, 0);
+                            tma_load_3d_pair(S.b[stage], &P.b_map[0], bar, b0, r, 0);
+                            if (half > 64) tma_load_3d_pair(S.b[stage] + 8192, &P.b_map[0], bar, b0 + 64, r, 0);
                         }
                         if (!kBMN) {
                             const int x = kb * (kF8 ? 128 : 64);
-                            if (half == 128) {
-                                tma_load_3d_pair(S.b[stage], &P.b_map, bar, x, b0, 0);
-                            } else {  // the ragged end: boxes of 16 rows
-                                for (int r = 0; r < half; r += 16)
-                                    tma_load_3d_pair(S.b[stage] + r * 128, &P.b_small, bar, x, b0 + r, 0);
-                            }
+                            // half rows in boxes of 128, 64, 32 and 16: few requests, no row too many
+                            int r = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (half & (128 >> i)) {
+                                    tma_load_3d_pair(S.b[stage] + r * 128, &P.b_map[i], bar, x, b0 + r, 0);
+                                    r += 128 >> i;
+                                }
                         }
                         issued |= 1u << stage;
                         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
@@ -397,7 +515,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             if (leader)
                 for (int s = 0; s < kGgStages; ++s)
                     if ((issued >> s) & 1u) mbar_wait_bounded(&S.full[s], (issued_par >> s) & 1u, 1u << 26, err);
-        } else if (warp == 1 && lane == 0 && leader) {
+        } else if (warp == 1 && leader && elect_one()) {
             // -------------------------------------------- MMA issuer (leader only)
             constexpr uint32_t type = kF8 ? 0u : 1u;  // e4m3 : bf16
             constexpr uint32_t idesc0 = (1u << 4) | (type << 7) | (type << 10) | ((kAMN ? 1u : 0u) << 15) |
@@ -409,14 +527,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             for (int t = pair; t < ntiles && ok; t += npairs) {
                 const GgTile ti = decode<OP>(P, S, t, e);
                 const uint32_t idesc = idesc0 | ((uint32_t)(ti.neff >> 3) << 17);
-                const int ck = kF8 ? 1 : P.chunk_kb;
+                const int ck = kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
                 for (int kb0 = 0; kb0 < ti.nkb && ok; kb0 += ck) {
-                    if (!mbar_wait_bounded(&S.cempty[buf], bphase ^ 1u, P.spin, err)) {
+                    if (!mbar_wait_bounded_cluster(&S.cempty[buf], bphase ^ 1u, P.spin, err)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t d = tmem_base + (uint32_t)(buf * kGgBN);
+                    uint32_t d = tmem_base + (uint32_t)(buf * kGgBN);
                     const int kb1 = min(ti.nkb, kb0 + ck);
                     for (int kb = kb0; kb < kb1; ++kb) {
                         if (!mbar_wait_bounded(&S.full[stage], phase, P.spin, err)) {
@@ -436,7 +554,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                         const uint64_t bd = kBMN ? sdesc_mn_sw128(sb) : sdesc_sw128(sb);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_pair<kF8>(d, ad + kk * a_step, bd + kk * b_step, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+                            umma_pair<kF8>(d, ad + kk * a_step, bd + kk * b_step, idesc,
+                                           ((!kF8 && kb > kb0) || kk > 0) ? 1u : 0u);
+                        if (kF8) d += (uint32_t)ti.neff;
                         umma_commit_pair_both(&S.empty[stage]);
                         if (++stage == kGgStages) {
                             stage = 0;
@@ -466,33 +586,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                 const int fb = ti.feat0 / 128 + (int)rank;
                 const float* sw = P.a_scale + ((long long)ti.e * fblocks + min(fb, fblocks - 1)) * kblocks;
                 for (int kb0 = 0; kb0 < ti.nkb; kb0 += kScaleBatch) {
-                    if (!mbar_wait_bounded(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
-                        ok = false;
-                        break;
-                    }
+                    // all loads of the batch in flight at once, and under the wait
                     float w[kScaleBatch];
+                    float4 v[kGgBN / 64];
 #pragma unroll
                     for (int q = 0; q < kScaleBatch; ++q) w[q] = kb0 + q < kblocks ? __ldg(sw + kb0 + q) : 0.f;
 #pragma unroll
                     for (int i = 0; i < kGgBN / 64; ++i) {
                         const int c = tid + 64 * i;
-                        if (c >= ti.neff) break;
-                        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (c < ti.ncols) {
-                            const float* p = P.b_scale + (long long)(ti.row0 + c) * kblocks + kb0;
-                            if (wide) {
-                                s = __ldg(reinterpret_cast<const float4*>(p));
-                            } else {
-                                s.x = __ldg(p);
-                                if (kb0 + 1 < kblocks) s.y = __ldg(p + 1);
-                                if (kb0 + 2 < kblocks) s.z = __ldg(p + 2);
-                                if (kb0 + 3 < kblocks) s.w = __ldg(p + 3);
-                            }
+                        const bool in = c < ti.ncols;
+                        const float* p = P.b_scale + (long long)(ti.row0 + (in ? c : 0)) * kblocks + kb0;
+                        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (wide) {
+                            if (in) v[i] = __ldg(reinterpret_cast<const float4*>(p));
+                        } else {
+                            if (in) v[i].x = __ldg(p);
+                            if (in && kb0 + 1 < kblocks) v[i].y = __ldg(p + 1);
+                            if (in && kb0 + 2 < kblocks) v[i].z = __ldg(p + 2);
+                            if (in && kb0 + 3 < kblocks) v[i].w = __ldg(p + 3);
                         }
-                        S.scale[buf][0][c] = s.x * w[0];
-                        S.scale[buf][1][c] = s.y * w[1];
-                        S.scale[buf][2][c] = s.z * w[2];
-                        S.scale[buf][3][c] = s.w * w[3];
+                    }
+                    if (!mbar_wait_bounded(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kGgBN / 64; ++i) {
+                        const int c = tid + 64 * i;
+                        if (c < ti.neff) {
+                            S.scale[buf][0][c] = v[i].x * w[0];
+                            S.scale[buf][1][c] = v[i].y * w[1];
+                            S.scale[buf][2][c] = v[i].z * w[2];
+                            S.scale[buf][3][c] = v[i].w * w[3];
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.sfull[buf]);
@@ -524,6 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                     copy_partial(S.a[stage], P.x, P.ldx, row, ti.rem, ti.feat0 + (int)rank * 128, P.feat, 128, tid);
                     copy_partial(S.b[stage], P.dy, P.lddy, row, ti.rem, ti.col0 + (int)rank * half, P.cols,
                                  (half + 63) & ~63, tid);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(mapa_shared(&S.tail[stage], 0));
@@ -541,10 +668,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         for (int t = pair; t < ntiles && ok; t += npairs) {
             const GgTile ti = decode<OP>(P, S, t, e);
             const int hc = ti.neff / 2, c0 = h * hc;  // this warp's accumulator columns c0 .. c0 + hc
-            uint64_t acc[64];
+            Acc acc;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-            const int ck = kF8 ? 1 : P.chunk_kb;
+            for (int i = 0; i < 16; ++i) acc[0][i][0] = acc[0][i][1] = acc[1][i][0] = acc[1][i][1] = 0ull;
+            const int ck = kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
+            const int ng = (hc + 31) >> 5;  // 32-column groups; an odd 16 reads 16 columns that are not stored
             for (int kb0 = 0; kb0 < ti.nkb; kb0 += ck) {
                 if (kF8 && kb0 % kScaleBatch == 0 && !mbar_wait_bounded(&S.sfull[sbuf], sphase, P.spin, err)) {
                     ok = false;
@@ -555,52 +683,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                     break;
                 }
                 tc_fence_after();
-                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGgBN + c0);
-                const float* sc = &S.scale[sbuf][kb0 % kScaleBatch][c0];
+                uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGgBN + c0);
+                const float* sc = &S.scale[sbuf][kb0 % kScaleBatch][c0 + 2 * (lane & 3)];
+                const int parts = kF8 ? min(ck, ti.nkb - kb0) : 1;
+                for (int part = 0; part < parts; ++part) {
+                    // the next group's loads run under this group's additions
+                    uint32_t raw[2][32];
+                    tmem_ld_16x32(taddr, &raw[0][0]);
+                    tmem_ld_16x32(taddr + (16u << 16), &raw[0][16]);
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    if (c < hc) {
-                        uint32_t r0[16], r1[16];
-                        tmem_ld16(taddr + (uint32_t)c, r0);
-                        if (c + 16 < hc) tmem_ld16(taddr + (uint32_t)(c + 16), r1);
-                        tmem_ld_wait();
-                        if (kF8) {
-#pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                const float4 s = *reinterpret_cast<const float4*>(sc + c + i);
-                                uint64_t* a = &acc[(c + i) / 2];
-                                a[0] = fma2(pack2(r0[i], r0[i + 1]), pack2(__float_as_uint(s.x), __float_as_uint(s.y)), a[0]);
-                                a[1] = fma2(pack2(r0[i + 2], r0[i + 3]), pack2(__float_as_uint(s.z), __float_as_uint(s.w)), a[1]);
+                    for (int g = 0; g < 4; ++g) {
+                        if (g < ng) {
+                            uint32_t* r = raw[g & 1];
+                            tmem_ld_wait32(r);
+                            if (g + 1 < ng) {
+                                tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
+                                tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)) + (16u << 16), &raw[(g + 1) & 1][16]);
+                            } else if (part == parts - 1) {  // all read: the buffer goes back before the last additions
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive_cluster_bare(mapa_shared(&S.cempty[buf], 0));
                             }
-                            if (c + 16 < hc) {
 #pragma unroll
-                                for (int i = 0; i < 16; i += 4) {
-                                    const float4 s = *reinterpret_cast<const float4*>(sc + c + 16 + i);
-                                    uint64_t* a = &acc[(c + 16 + i) / 2];
-                                    a[0] = fma2(pack2(r1[i], r1[i + 1]), pack2(__float_as_uint(s.x), __float_as_uint(s.y)), a[0]);
-                                    a[1] = fma2(pack2(r1[i + 2], r1[i + 3]), pack2(__float_as_uint(s.z), __float_as_uint(s.w)), a[1]);
+                            for (int b = 0; b < 4; ++b) {
+                                if (kF8) {
+                                    const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + 32 * g + 8 * b);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        uint64_t& a = acc[i >> 1][4 * g + b][i & 1];
+                                        const uint32_t* v = r + 16 * (i >> 1) + 4 * b + 2 * (i & 1);
+                                        a = fma2(pack2(v[0], v[1]), s2, a);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        uint64_t& a = acc[i >> 1][4 * g + b][i & 1];
+                                        const uint32_t* v = r + 16 * (i >> 1) + 4 * b + 2 * (i & 1);
+                                        a = add2(a, pack2(v[0], v[1]));
+                                    }
                                 }
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                acc[c / 2 + i] = add2(acc[c / 2 + i], pack2(r0[2 * i], r0[2 * i + 1]));
-                            if (c + 16 < hc) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    acc[c / 2 + 8 + i] = add2(acc[c / 2 + 8 + i], pack2(r1[2 * i], r1[2 * i + 1]));
                             }
                         }
                     }
+                    if (kF8) {
+                        taddr += (uint32_t)ti.neff;
+                        sc += kGgBN;
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(&S.cempty[buf], 0));
                 if (++buf == 2) {
                     buf = 0;
                     bphase ^= 1u;
                 }
-                if (kF8 && (kb0 % kScaleBatch == kScaleBatch - 1 || kb0 == ti.nkb - 1)) {
+                if (kF8 && ((kb0 + ck) % kScaleBatch == 0 || kb0 + ck >= ti.nkb)) {
+                    __syncwarp();
                     if (lane == 0) mbar_arrive(&S.sempty[sbuf]);
                     if (++sbuf == 2) {
                         sbuf = 0;
@@ -609,34 +744,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                 }
             }
             if (!ok) break;
-            // lanes hold consecutive features: 64 (bf16) or 128 (fp32) contiguous bytes per row and warp
-            const int f = ti.feat0 + (int)rank * 128 + q * 32 + lane;
-            const int nv = f < P.feat ? min(hc, ti.ncols - c0) : 0;
+            const int f = ti.feat0 + (int)rank * 128 + q * 32;
+            const int nv = min(hc, ti.ncols - c0);
             const long long first = OP == GG_DW ? (long long)ti.e * P.cols + ti.col0 + c0 : (long long)ti.row0 + c0;
-            const long long at = first * P.ldo + f;
-            if (P.out_f32) {
-                float* o = static_cast<float*>(P.out) + at;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    float lo, hi;
-                    unpack2(acc[i], lo, hi);
-                    if (2 * i < nv) *o = lo;
-                    o += P.ldo;
-                    if (2 * i + 1 < nv) *o = hi;
-                    o += P.ldo;
-                }
-            } else {
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(P.out) + at;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    float lo, hi;
-                    unpack2(acc[i], lo, hi);
-                    if (2 * i < nv) *o = __float2bfloat16_rn(lo);
-                    o += P.ldo;
-                    if (2 * i + 1 < nv) *o = __float2bfloat16_rn(hi);
-                    o += P.ldo;
-                }
-            }
+            if (f < P.feat)
+                store_rows(acc, S.stage[warp - 4], static_cast<char*>(P.out) + (first * P.ldo + f) * (P.out_f32 ? 4 : 2),
+                           P.ldo, nv, P.feat - f, P.out_f32, lane);
         }
     }
     __syncthreads();

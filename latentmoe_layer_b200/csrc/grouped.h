@@ -9,8 +9,7 @@ enum GgOp : int { GG_FWD = 0, GG_DX = 1, GG_DW = 2, GG_FP8 = 3 };
 
 struct alignas(64) GgParams {
     CUtensorMap a_map;    // feature-side operand
-    CUtensorMap b_map;    // row-side operand, boxes of 128 rows (GG_DW: 64 x 64)
-    CUtensorMap b_small;  // row-side operand, boxes of 16 rows (not GG_DW)
+    CUtensorMap b_map[4]; // row-side operand, boxes of 128, 64, 32 and 16 rows (GG_DW: the first, 64 x 64)
     const int* counts;    // [n_groups] rows per group; null: one group of n_rows rows
     const float* a_scale; // GG_FP8: [n_groups, ceil(feat / 128), ceil(cdim / 128)]
     const float* b_scale; // GG_FP8: [n_rows, ceil(cdim / 128)]

@@ -86,6 +86,13 @@ bool encode(const OpsState& st, CUtensorMap* m, const void* base, bool bf16, lon
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The row-side operand [n_rows, cols] in boxes of 128, 64, 32 and 16 rows.
+bool encode_rows(const OpsState& st, GgParams& P, const void* base, bool bf16, int n_rows, int cols, long long pitch) {
+    for (int i = 0; i < 4; ++i)
+        if (!encode(st, &P.b_map[i], base, bf16, 1, n_rows, cols, pitch, 128 >> i)) return false;
+    return true;
+}
+
 constexpr long long kMaxDim = 1LL << 24;        // N, K
 constexpr long long kMaxElems = 1LL << 38;      // elements of one operand
 constexpr long long kMaxTiles = 1LL << 30;      // tiles of one launch
@@ -151,8 +158,7 @@ lmoe_status run_rows(bool dx, const void* a, long long lda, const void* w, const
     P.cdim = in_cols;
     P.zero_tail = zero_tail != 0;
     if (!encode(*st, &P.a_map, w, true, n_groups, N, K, K, dx ? 64 : 128) ||
-        !encode(*st, &P.b_map, a, true, 1, n_rows, in_cols, lda, 128) ||
-        !encode(*st, &P.b_small, a, true, 1, n_rows, in_cols, lda, 16))
+        !encode_rows(*st, P, a, true, n_rows, in_cols, lda))
         return LMOE_ERR_CUDA;
     return cuda_status(launch_grouped(dx ? GG_DX : GG_FWD, P, static_cast<cudaStream_t>(stream)));
 }
@@ -196,7 +202,7 @@ lmoe_status latentmoe_grouped_gemm_dw(const void* dy, long long lddy, const void
     P.ldo = K;
     P.feat = K;
     P.cols = N;
-    if (!encode(*st, &P.a_map, x, true, 1, n_rows, K, ldx, 64) || !encode(*st, &P.b_map, dy, true, 1, n_rows, N, lddy, 64))
+    if (!encode(*st, &P.a_map, x, true, 1, n_rows, K, ldx, 64) || !encode(*st, &P.b_map[0], dy, true, 1, n_rows, N, lddy, 64))
         return LMOE_ERR_CUDA;
     return cuda_status(launch_grouped(GG_DW, P, static_cast<cudaStream_t>(stream)));
 }
@@ -237,7 +243,7 @@ lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, 
     P.cdim = K;
     P.zero_tail = zero_tail != 0;
     if (!encode(*st, &P.a_map, wq, false, n_groups, N, K, K, 128) ||
-        !encode(*st, &P.b_map, xq, false, 1, n_rows, K, K, 128) || !encode(*st, &P.b_small, xq, false, 1, n_rows, K, K, 16))
+        !encode_rows(*st, P, xq, false, n_rows, K, K))
         return LMOE_ERR_CUDA;
     return cuda_status(launch_grouped(GG_FP8, P, static_cast<cudaStream_t>(stream)));
 }
