@@ -66,9 +66,13 @@ constexpr int kGgThreads = 384;
 constexpr int kGgEpiWarps = 8;
 constexpr int kGgRaster = 8;          // N-side tiles per raster block (shared weight reads in L2)
 constexpr int kScaleBatch = 4;        // k-blocks per batch of scale products
-// registers per thread: 128 x kProdRegs + 256 x kEpiRegs must not exceed 384 x kLaunchRegs
-constexpr int kLaunchRegs = 168, kProdRegs = 72, kEpiRegs = 216;
-static_assert(128 * kProdRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "register split");
+// Registers per thread: 128 x producers' + 256 x epilogue's must not exceed 384 x kLaunchRegs.
+constexpr int kLaunchRegs = 168;
+template <int OP>
+struct GgRegs {
+    static constexpr int kProd = OP == GG_FP8 ? 72 : 56, kEpi = OP == GG_FP8 ? 216 : 224;
+    static_assert(128 * kProd + 256 * kEpi <= 384 * kLaunchRegs, "register split");
+};
 
 struct alignas(1024) GgShared {
     uint8_t a[kGgStages][kGgABytes];
@@ -180,7 +184,7 @@ __device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, i
     const int cnt = S.off[e + 1] - S.off[e];
     // a group's rows are spread evenly over its tiles (in steps of 32): pairs take tiles in
     // turn, so a full tile here and a short one there would leave some pairs waiting
-    const int per = OP == GG_DW ? kGgBN : (ceil_div(cnt, ct) + 31) & ~31;
+    const int per = OP == GG_DW || OP == GG_FP8_ROWS ? kGgBN : (ceil_div(cnt, ct) + 31) & ~31;
     GgTile ti;
     ti.e = e;
     ti.feat0 = (r / ms) * 256;
@@ -194,10 +198,10 @@ __device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, i
         ti.row0 = S.off[e] + c * per;
         ti.col0 = 0;
         ti.ncols = min(per, cnt - c * per);
-        ti.nkb = e < P.n_groups ? ceil_div(P.cdim, OP == GG_FP8 ? 128 : 64) : 0;
+        ti.nkb = e < P.n_groups ? ceil_div(P.cdim, OP == GG_FP8 || OP == GG_FP8_ROWS ? 128 : 64) : 0;
         ti.rem = 0;
     }
-    ti.neff = (ti.ncols + 31) & ~31;
+    ti.neff = ((OP == GG_FP8_ROWS ? min(kGgBN, P.feat - ti.feat0) : ti.ncols) + 31) & ~31;
     return ti;
 }
 
@@ -414,9 +418,185 @@ __device__ __forceinline__ void store_rows(const Acc& acc, uint8_t* stage, void*
     }
 }
 
+// Adds 32 lanes x 32 NG columns of TMEM to acc, GG_FP8 with a factor per column at sc (the
+// thread's first pair of columns); gives the buffer back after the last load of the
+// `last` part. Loads run one group ahead; NG as in drain_rows.
+template <int NG, bool kF8>
+__device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const float* sc, bool last, uint32_t release,
+                                              int lane) {
+    uint32_t raw[2][32];
+    tmem_ld_16x32(taddr, &raw[0][0]);
+    tmem_ld_16x32(taddr + (16u << 16), &raw[0][16]);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        uint32_t* r = raw[g & 1];
+        tmem_ld_wait32(r);
+        if (g + 1 < NG) {
+            tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
+            tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)) + (16u << 16), &raw[(g + 1) & 1][16]);
+        } else if (last) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_bare(release);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const uint64_t s2 = kF8 ? *reinterpret_cast<const uint64_t*>(sc + 32 * g + 8 * b) : 0ull;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint64_t& a = acc[i >> 1][4 * g + b][i & 1];
+                const uint32_t* v = r + 16 * (i >> 1) + 4 * b + 2 * (i & 1);
+                a = kF8 ? fma2(pack2(v[0], v[1]), s2, a) : add2(a, pack2(v[0], v[1]));
+            }
+        }
+    }
+}
+
+// 32 TMEM lanes x 16 columns: register i holds the thread's lane, column i.
+__device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Four consecutive k-blocks' scales of one operand row (zero past the end).
+__device__ __forceinline__ float4 load_scales(const float* p, int left, bool wide) {
+    if (wide) return __ldg(reinterpret_cast<const float4*>(p));
+    float4 s = make_float4(__ldg(p), 0.f, 0.f, 0.f);
+    if (left > 1) s.y = __ldg(p + 1);
+    if (left > 2) s.z = __ldg(p + 2);
+    if (left > 3) s.w = __ldg(p + 3);
+    return s;
+}
+
+// Adds s x (32 lanes x 32 NG columns of TMEM) to acc and gives the buffer back when
+// the last load has arrived. Loads run one group ahead of the additions. (NG is a
+// template argument because conditions between the groups cost moves of the
+// registers in flight.)
+template <int NG>
+__device__ __forceinline__ void drain_rows(float (&acc)[128], uint32_t taddr, float s, uint32_t release, int lane) {
+    uint32_t raw[2][32];
+    tmem_ld_32x16(taddr, &raw[0][0]);
+    tmem_ld_32x16(taddr + 16, &raw[0][16]);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        uint32_t* r = raw[g & 1];
+        tmem_ld_wait32(r);
+        if (g + 1 < NG) {
+            tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
+            tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1) + 16), &raw[(g + 1) & 1][16]);
+        } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_bare(release);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[32 * g + i] = fmaf(__uint_as_float(r[i]), s, acc[32 * g + i]);
+    }
+}
+
+// GG_FP8_ROWS: a warp holds 32 rows (a lane each) x 128 features of one weight
+// block, so a 128-deep block's factor sx * sw is one register per thread and the
+// drain touches no shared memory, whose bandwidth the MMA's operands use up.
+__device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, int pair, int npairs, int ntiles,
+                                              uint32_t rank, int q, int h, int lane, uint32_t tmem_base) {
+    const int kblocks = ceil_div(P.cdim, 128), fblocks = ceil_div(P.feat, 128);
+    const bool wide = (kblocks & 3) == 0;  // rows of scales are 16-byte aligned
+    int buf = 0, e = 0;
+    uint32_t bphase = 0;
+    for (int t = pair; t < ntiles; t += npairs) {
+        const GgTile ti = decode<GG_FP8_ROWS>(P, S, t, e);
+        const int row = (int)rank * 128 + q * 32 + lane;               // of the tile
+        const int c0 = h * 128, hc = min(128, max(0, ti.neff - c0));   // the warp's columns
+        const int ng = (hc + 31) >> 5;
+        const float* sx = P.b_scale + (long long)(ti.row0 + min(row, ti.ncols - 1)) * kblocks;
+        const float* sw = P.a_scale + ((long long)ti.e * fblocks + min(ti.feat0 / 128 + h, fblocks - 1)) * kblocks;
+        float acc[128];
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        float4 nx = make_float4(0.f, 0.f, 0.f, 0.f), nw = nx;
+        if (ti.nkb > 0) {
+            nx = load_scales(sx, kblocks, wide);
+            nw = load_scales(sw, kblocks, wide);
+        }
+        float4 f = nx;
+        for (int kb = 0; kb < ti.nkb; ++kb) {
+            if ((kb & 3) == 0) {
+                f = make_float4(nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w);
+                if (kb + 4 < ti.nkb) {  // the next four, under this batch
+                    nx = load_scales(sx + kb + 4, kblocks - kb - 4, wide);
+                    nw = load_scales(sw + kb + 4, kblocks - kb - 4, wide);
+                }
+            }
+            const float s = f.x;
+            f = make_float4(f.y, f.z, f.w, 0.f);
+            if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
+            tc_fence_after();
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGgBN + c0);
+            const uint32_t release = mapa_shared(&S.cempty[buf], 0);
+            switch (ng) {
+                case 4: drain_rows<4>(acc, taddr, s, release, lane); break;
+                case 3: drain_rows<3>(acc, taddr, s, release, lane); break;
+                case 2: drain_rows<2>(acc, taddr, s, release, lane); break;
+                case 1: drain_rows<1>(acc, taddr, s, release, lane); break;
+                default:
+                    if (lane == 0) mbar_arrive_cluster_bare(release);
+            }
+            if (++buf == 2) {
+                buf = 0;
+                bphase ^= 1u;
+            }
+        }
+        // rows of 64 features (bf16) or 32 (fp32), 4 rows x 128 bytes per store through shared memory:
+        // the warp's 2 KB hold 16 rows of 128 bytes, pieces swizzled by the row's index modulo 8
+        const int nrows = min(32, ti.ncols - ((int)rank * 128 + q * 32));  // may be <= 0
+        uint8_t* st = S.stage[q + 4 * h];
+        const int esz = P.out_f32 ? 4 : 2, per = 128 / esz;
+        char* out = static_cast<char*>(P.out) +
+                    ((long long)(ti.row0 + (int)rank * 128 + q * 32) * P.ldo + ti.feat0 + c0) * esz;
+        const int feats = P.feat - ti.feat0 - c0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {  // 128 bytes of every row
+            if ((P.out_f32 || g < 2) && g * per < feats) {
+#pragma unroll
+                for (int hr = 0; hr < 2; ++hr) {  // 16 of the warp's rows
+                    if ((lane >> 4) == hr) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            uint4 v;
+                            if (P.out_f32) {
+                                const float* a = acc + 32 * g + 4 * c;
+                                v = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                                               __float_as_uint(a[3]));
+                            } else {
+                                const float* a = acc + 64 * (g & 1) + 8 * c;
+                                v = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                               pack_bf16x2(a[6], a[7]));
+                            }
+                            *reinterpret_cast<uint4*>(st + (lane & 15) * 128 + ((c ^ (lane & 7)) << 4)) = v;
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = (lane >> 3) + 4 * i, c = lane & 7;
+                        const uint4 v = ld_shared_v4(st + r * 128 + ((c ^ (r & 7)) << 4));
+                        if (hr * 16 + r < nrows && g * per + c * (16 / esz) < feats)
+                            *reinterpret_cast<uint4*>(out + ((long long)(hr * 16 + r) * P.ldo) * esz + g * 128 + c * 16) = v;
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    }
+}
+
 template <int OP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant__ GgParams P) {
-    constexpr bool kF8 = OP == GG_FP8, kAMN = OP == GG_DX || OP == GG_DW, kBMN = OP == GG_DW;
+    constexpr bool kF8 = OP == GG_FP8 || OP == GG_FP8_ROWS, kRowsM = OP == GG_FP8_ROWS, kAMN = OP == GG_DX || OP == GG_DW, kBMN = OP == GG_DW;
     extern __shared__ uint8_t smem_raw[];
     GgShared& S = *reinterpret_cast<GgShared*>(smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw)));
 
@@ -454,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
     int* err = P.err;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProdRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GgRegs<OP>::kProd));
         if (warp == 0 && elect_one()) {
             // -------------------------------------------- TMA producer (both CTAs)
             int stage = 0, e = 0;
@@ -464,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                 const GgTile ti = decode<OP>(P, S, t, e);
                 const int half = ti.neff / 2, f0 = ti.feat0 + (int)rank * 128;
                 const int b0 = (kBMN ? ti.col0 : ti.row0) + (int)rank * half;
-                const uint32_t bytes_b = kBMN ? (uint32_t)((half + 63) / 64) * 8192u : (uint32_t)half * 128u;
+                const uint32_t bytes_b = kRowsM ? (uint32_t)kGgBBytes : kBMN ? (uint32_t)((half + 63) / 64) * 8192u : (uint32_t)half * 128u;
                 for (int kb = 0; kb < ti.nkb; ++kb) {
                     if (!mbar_wait_bounded(&S.empty[stage], phase ^ 1u, P.spin, err)) {
                         ok = false;
@@ -478,7 +658,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                     } else {
                         if (leader) mbar_arrive_expect_tx(&S.full[stage], 2u * (kGgABytes + bytes_b));
                         const uint32_t bar = mapa_shared(&S.full[stage], 0);
-                        if (OP == GG_FWD || OP == GG_FP8) {
+                        if (kRowsM) {
+                            tma_load_3d_pair(S.a[stage], &P.b_map[0], bar, kb * 128, ti.row0 + (int)rank * 128, 0);
+                            tma_load_3d_pair(S.b[stage], &P.a_map, bar, kb * 128, ti.feat0 + (int)rank * half, ti.e);
+                        } else if (OP == GG_FWD || OP == GG_FP8) {
                             tma_load_3d_pair(S.a[stage], &P.a_map, bar, kb * (kF8 ? 128 : 64), f0, ti.e);
                         } else if (OP == GG_DX) {
                             tma_load_3d_pair(S.a[stage], &P.a_map, bar, f0, kb * 64, ti.e);
@@ -490,7 +673,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                             tma_load_3d_pair(S.b[stage], &P.b_map[0], bar, b0, r, 0);
                             if (half > 64) tma_load_3d_pair(S.b[stage] + 8192, &P.b_map[0], bar, b0 + 64, r, 0);
                         }
-                        if (!kBMN) {
+                        if (!kBMN && !kRowsM) {
                             const int x = kb * (kF8 ? 128 : 64);
                             // half rows in boxes of 128, 64, 32 and 16: few requests, no row too many
                             int r = 0;
@@ -527,7 +710,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             for (int t = pair; t < ntiles && ok; t += npairs) {
                 const GgTile ti = decode<OP>(P, S, t, e);
                 const uint32_t idesc = idesc0 | ((uint32_t)(ti.neff >> 3) << 17);
-                const int ck = kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
+                const int ck = kRowsM ? 1 : kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
                 for (int kb0 = 0; kb0 < ti.nkb && ok; kb0 += ck) {
                     if (!mbar_wait_bounded_cluster(&S.cempty[buf], bphase ^ 1u, P.spin, err)) {
                         ok = false;
@@ -573,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             }
             umma_commit_pair_self(&S.done);
             mbar_wait_bounded(&S.done, 0, 1u << 26, err);
-        } else if (warp >= 2 && kF8) {
+        } else if (warp >= 2 && OP == GG_FP8) {
             // -------------------------------------------- scale products
             const int tid = threadIdx.x - 64;
             const int kblocks = ceil_div(P.cdim, 128), fblocks = ceil_div(P.feat, 128);
@@ -660,8 +843,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         }
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GgRegs<OP>::kEpi));
         const int q = warp & 3, h = (warp - 4) >> 2;
+        if (kRowsM) {
+            epilogue_rows(P, S, pair, npairs, ntiles, rank, q, h, lane, tmem_base);
+        } else {
         int buf = 0, sbuf = 0, e = 0;
         uint32_t bphase = 0, sphase = 0;
         bool ok = true;
@@ -686,44 +872,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                 uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGgBN + c0);
                 const float* sc = &S.scale[sbuf][kb0 % kScaleBatch][c0 + 2 * (lane & 3)];
                 const int parts = kF8 ? min(ck, ti.nkb - kb0) : 1;
+                const uint32_t release = mapa_shared(&S.cempty[buf], 0);
                 for (int part = 0; part < parts; ++part) {
-                    // the next group's loads run under this group's additions
-                    uint32_t raw[2][32];
-                    tmem_ld_16x32(taddr, &raw[0][0]);
-                    tmem_ld_16x32(taddr + (16u << 16), &raw[0][16]);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        if (g < ng) {
-                            uint32_t* r = raw[g & 1];
-                            tmem_ld_wait32(r);
-                            if (g + 1 < ng) {
-                                tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
-                                tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)) + (16u << 16), &raw[(g + 1) & 1][16]);
-                            } else if (part == parts - 1) {  // all read: the buffer goes back before the last additions
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive_cluster_bare(mapa_shared(&S.cempty[buf], 0));
-                            }
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                if (kF8) {
-                                    const uint64_t s2 = *reinterpret_cast<const uint64_t*>(sc + 32 * g + 8 * b);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        uint64_t& a = acc[i >> 1][4 * g + b][i & 1];
-                                        const uint32_t* v = r + 16 * (i >> 1) + 4 * b + 2 * (i & 1);
-                                        a = fma2(pack2(v[0], v[1]), s2, a);
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        uint64_t& a = acc[i >> 1][4 * g + b][i & 1];
-                                        const uint32_t* v = r + 16 * (i >> 1) + 4 * b + 2 * (i & 1);
-                                        a = add2(a, pack2(v[0], v[1]));
-                                    }
-                                }
-                            }
-                        }
+                    const bool last = part == parts - 1;
+                    switch (ng) {
+                        case 4: drain_columns<4, kF8>(acc, taddr, sc, last, release, lane); break;
+                        case 3: drain_columns<3, kF8>(acc, taddr, sc, last, release, lane); break;
+                        case 2: drain_columns<2, kF8>(acc, taddr, sc, last, release, lane); break;
+                        default: drain_columns<1, kF8>(acc, taddr, sc, last, release, lane);
                     }
                     if (kF8) {
                         taddr += (uint32_t)ti.neff;
@@ -750,6 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             if (f < P.feat)
                 store_rows(acc, S.stage[warp - 4], static_cast<char*>(P.out) + (first * P.ldo + f) * (P.out_f32 ? 4 : 2),
                            P.ldo, nv, P.feat - f, P.out_f32, lane);
+        }
         }
     }
     __syncthreads();
@@ -797,6 +954,7 @@ cudaError_t launch_grouped(int op, const GgParams& P, cudaStream_t s) {
         case GG_DX: return launch_op<GG_DX>(P, (int)pairs, s);
         case GG_DW: return launch_op<GG_DW>(P, (int)pairs, s);
         case GG_FP8: return launch_op<GG_FP8>(P, (int)pairs, s);
+        case GG_FP8_ROWS: return launch_op<GG_FP8_ROWS>(P, (int)pairs, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -5,7 +5,7 @@
 
 namespace lmoe {
 
-enum GgOp : int { GG_FWD = 0, GG_DX = 1, GG_DW = 2, GG_FP8 = 3 };
+enum GgOp : int { GG_FWD = 0, GG_DX = 1, GG_DW = 2, GG_FP8 = 3, GG_FP8_ROWS = 4 };
 
 struct alignas(64) GgParams {
     CUtensorMap a_map;    // feature-side operand

@@ -245,7 +245,8 @@ lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, 
     if (!encode(*st, &P.a_map, wq, false, n_groups, N, K, K, 128) ||
         !encode_rows(*st, P, xq, false, n_rows, K, K))
         return LMOE_ERR_CUDA;
-    return cuda_status(launch_grouped(GG_FP8, P, static_cast<cudaStream_t>(stream)));
+    const int op = n_rows / n_groups > 64 ? GG_FP8_ROWS : GG_FP8;
+    return cuda_status(launch_grouped(op, P, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
