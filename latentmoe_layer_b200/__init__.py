@@ -213,7 +213,16 @@ def latentmoe_selftest_bounded_wait(h) -> int:
 
 
 # ---------------------------------------------------------------- products without a handle
-from .ops import gemm_fp8, grouped_gemm, grouped_gemm_dw, grouped_gemm_dx, quantize_fp8  # noqa: E402,F401
+_PRODUCTS = ("grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw", "quantize_fp8", "gemm_fp8")
+
+
+def __getattr__(name):
+    """The products are torch functions: their module, and with it torch, is imported at first use."""
+    if name in _PRODUCTS:
+        from . import ops
+        globals().update({n: getattr(ops, n) for n in _PRODUCTS})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 # ---------------------------------------------------------------- convenience wrapper

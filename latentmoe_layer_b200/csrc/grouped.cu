@@ -246,12 +246,18 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
     return d;
 }
 
-// Arrive on another CTA's barrier without its release at cluster scope: that would
-// first wait for the thread's own stores to global memory (1.3K to 3.7K cycles per
+// Arrive (where `on`) on a barrier of either CTA of the pair without a release: that
+// would first wait for the thread's own stores to global memory (1.3K to 3.7K cycles per
 // hand-over of a TMEM buffer). Nothing this thread wrote is handed over here: its
-// TMEM loads have completed (tcgen05.wait::ld, tcgen05.fence).
-__device__ __forceinline__ void mbar_arrive_cluster_bare(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// TMEM or shared-memory reads have completed. Predicated, so that the warp does
+// not branch.
+__device__ __forceinline__ void mbar_arrive_bare(uint32_t cluster_addr, bool on) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+        "r"((uint32_t)on)
+        : "memory");
 }
 
 // One lane of a converged warp; the compiler then knows the branch is uniform.
@@ -342,6 +348,16 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
                  :
                  : "memory");
 }
+// Four consecutive k-blocks' scales of one operand row, zero past its `left` last ones.
+__device__ __forceinline__ float4 load_scales(const float* p, int left, bool wide) {
+    if (wide) return __ldg(reinterpret_cast<const float4*>(p));
+    float4 s = make_float4(__ldg(p), 0.f, 0.f, 0.f);
+    if (left > 1) s.y = __ldg(p + 1);
+    if (left > 2) s.z = __ldg(p + 2);
+    if (left > 3) s.w = __ldg(p + 3);
+    return s;
+}
+
 // Four 8 x 8 matrices of 16-bit values, transposed on their way to shared memory.
 __device__ __forceinline__ void stmatrix_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
@@ -420,7 +436,8 @@ __device__ __forceinline__ void store_rows(const Acc& acc, uint8_t* stage, void*
 
 // Adds 32 lanes x 32 NG columns of TMEM to acc, GG_FP8 with a factor per column at sc (the
 // thread's first pair of columns); gives the buffer back after the last load of the
-// `last` part. Loads run one group ahead; NG as in drain_rows.
+// `last` part. Loads run one group ahead of the additions. (NG is a template argument
+// because conditions between the groups cost moves of the registers in flight.)
 template <int NG, bool kF8>
 __device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const float* sc, bool last, uint32_t release,
                                               int lane) {
@@ -437,7 +454,7 @@ __device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const fl
         } else if (last) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_bare(release);
+            mbar_arrive_bare(release, lane == 0);
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -462,88 +479,92 @@ __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t* r) {
         : "r"(taddr));
 }
 
-// Four consecutive k-blocks' scales of one operand row (zero past the end).
-__device__ __forceinline__ float4 load_scales(const float* p, int left, bool wide) {
-    if (wide) return __ldg(reinterpret_cast<const float4*>(p));
-    float4 s = make_float4(__ldg(p), 0.f, 0.f, 0.f);
-    if (left > 1) s.y = __ldg(p + 1);
-    if (left > 2) s.z = __ldg(p + 2);
-    if (left > 3) s.w = __ldg(p + 3);
-    return s;
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
-
-// Adds s x (32 lanes x 32 NG columns of TMEM) to acc and gives the buffer back when
-// the last load has arrived. Loads run one group ahead of the additions. (NG is a
-// template argument because conditions between the groups cost moves of the
-// registers in flight.)
-template <int NG>
-__device__ __forceinline__ void drain_rows(float (&acc)[128], uint32_t taddr, float s, uint32_t release, int lane) {
-    uint32_t raw[2][32];
-    tmem_ld_32x16(taddr, &raw[0][0]);
-    tmem_ld_32x16(taddr + 16, &raw[0][16]);
+__device__ __forceinline__ void add_group(float* acc, const uint32_t* r, float s) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        uint32_t* r = raw[g & 1];
-        tmem_ld_wait32(r);
-        if (g + 1 < NG) {
-            tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
-            tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1) + 16), &raw[(g + 1) & 1][16]);
-        } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_bare(release);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[32 * g + i] = fmaf(__uint_as_float(r[i]), s, acc[32 * g + i]);
-    }
+    for (int i = 0; i < 16; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
 }
 
 // GG_FP8_ROWS: a warp holds 32 rows (a lane each) x 128 features of one weight
 // block, so a 128-deep block's factor sx * sw is one register per thread and the
 // drain touches no shared memory, whose bandwidth the MMA's operands use up.
 __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, int pair, int npairs, int ntiles,
-                                              uint32_t rank, int q, int h, int lane, uint32_t tmem_base) {
-    const int kblocks = ceil_div(P.cdim, 128), fblocks = ceil_div(P.feat, 128);
-    const bool wide = (kblocks & 3) == 0;  // rows of scales are 16-byte aligned
-    int buf = 0, e = 0;
-    uint32_t bphase = 0;
+                                              uint32_t rank, int q, int h, int lane, uint32_t tmem_base, uint32_t cempty0) {
+    int buf = 0, sbuf = 0, e = 0, stage = 0;
+    uint32_t bphase = 0, sphase = 0;
+    const bool frees = q == 0 && h == 0 && lane == 0;
+    const uint32_t empty0 = mapa_shared(&S.empty[0], rank), sempty0 = mapa_shared(&S.sempty[0], rank);
+    auto free_stage = [&] {  // the block's operands have been read
+        mbar_arrive_bare(empty0 + 8u * (uint32_t)stage, frees);
+        if (++stage == kGgStages) stage = 0;
+    };
     for (int t = pair; t < ntiles; t += npairs) {
         const GgTile ti = decode<GG_FP8_ROWS>(P, S, t, e);
-        const int row = (int)rank * 128 + q * 32 + lane;               // of the tile
-        const int c0 = h * 128, hc = min(128, max(0, ti.neff - c0));   // the warp's columns
-        const int ng = (hc + 31) >> 5;
-        const float* sx = P.b_scale + (long long)(ti.row0 + min(row, ti.ncols - 1)) * kblocks;
-        const float* sw = P.a_scale + ((long long)ti.e * fblocks + min(ti.feat0 / 128 + h, fblocks - 1)) * kblocks;
+        const int c0 = h * 128, hc = min(128, max(0, ti.neff - c0));  // the warp's columns
         float acc[128];
 #pragma unroll
         for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        float4 nx = make_float4(0.f, 0.f, 0.f, 0.f), nw = nx;
-        if (ti.nkb > 0) {
-            nx = load_scales(sx, kblocks, wide);
-            nw = load_scales(sw, kblocks, wide);
-        }
-        float4 f = nx;
+        uint32_t raw[2][16];
+        float4 f;
         for (int kb = 0; kb < ti.nkb; ++kb) {
-            if ((kb & 3) == 0) {
-                f = make_float4(nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w);
-                if (kb + 4 < ti.nkb) {  // the next four, under this batch
-                    nx = load_scales(sx + kb + 4, kblocks - kb - 4, wide);
-                    nw = load_scales(sw + kb + 4, kblocks - kb - 4, wide);
+            if (kb % kScaleBatch == 0) {
+                if (!mbar_wait_bounded(&S.sfull[sbuf], sphase, P.spin, P.err)) return;
+                f = *reinterpret_cast<const float4*>(&S.scale[sbuf][0][0] + 4 * (h * 128 + q * 32 + lane));
+                __syncwarp();
+                mbar_arrive_bare(sempty0 + 8u * (uint32_t)sbuf, lane == 0);
+                if (++sbuf == 2) {
+                    sbuf = 0;
+                    sphase ^= 1u;
                 }
             }
             const float s = f.x;
             f = make_float4(f.y, f.z, f.w, 0.f);
-            if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
-            tc_fence_after();
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGgBN + c0);
-            const uint32_t release = mapa_shared(&S.cempty[buf], 0);
-            switch (ng) {
-                case 4: drain_rows<4>(acc, taddr, s, release, lane); break;
-                case 3: drain_rows<3>(acc, taddr, s, release, lane); break;
-                case 2: drain_rows<2>(acc, taddr, s, release, lane); break;
-                case 1: drain_rows<1>(acc, taddr, s, release, lane); break;
-                default:
-                    if (lane == 0) mbar_arrive_cluster_bare(release);
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
+            if (hc == 128) {
+                // the next block's first loads run under this one's last additions
+                if (kb == 0) {
+                    if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
+                    free_stage();
+                    tc_fence_after();
+                    tmem_ld_32x16(taddr + (uint32_t)(buf * kGgBN), raw[0]);
+                }
+#pragma unroll
+                for (int g = 0; g < 7; ++g) {
+                    tmem_ld_wait16(raw[g & 1]);
+                    tmem_ld_32x16(taddr + (uint32_t)(buf * kGgBN + 16 * (g + 1)), raw[(g + 1) & 1]);
+                    add_group(acc + 16 * g, raw[g & 1], s);
+                }
+                tmem_ld_wait16(raw[1]);
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_bare(cempty0 + 8u * (uint32_t)buf, lane == 0);
+                if (kb + 1 < ti.nkb) {
+                    if (!mbar_wait_bounded(&S.cfull[buf ^ 1], bphase ^ (uint32_t)buf, P.spin, P.err)) return;
+                    free_stage();
+                    tc_fence_after();
+                    tmem_ld_32x16(taddr + (uint32_t)((buf ^ 1) * kGgBN), raw[0]);
+                }
+                add_group(acc + 112, raw[1], s);
+            } else {
+                if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
+                free_stage();
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 6; ++g)
+                    if (16 * g < hc) {
+                        tmem_ld_32x16(taddr + (uint32_t)(buf * kGgBN + 16 * g), raw[0]);
+                        tmem_ld_wait16(raw[0]);
+                        add_group(acc + 16 * g, raw[0], s);
+                    }
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_bare(cempty0 + 8u * (uint32_t)buf, lane == 0);
             }
             if (++buf == 2) {
                 buf = 0;
@@ -712,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                 const uint32_t idesc = idesc0 | ((uint32_t)(ti.neff >> 3) << 17);
                 const int ck = kRowsM ? 1 : kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
                 for (int kb0 = 0; kb0 < ti.nkb && ok; kb0 += ck) {
-                    if (!mbar_wait_bounded_cluster(&S.cempty[buf], bphase ^ 1u, P.spin, err)) {
+                    if (!mbar_wait_bounded(&S.cempty[buf], bphase ^ 1u, P.spin, err)) {
                         ok = false;
                         break;
                     }
@@ -740,7 +761,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                             umma_pair<kF8>(d, ad + kk * a_step, bd + kk * b_step, idesc,
                                            ((!kF8 && kb > kb0) || kk > 0) ? 1u : 0u);
                         if (kF8) d += (uint32_t)ti.neff;
-                        umma_commit_pair_both(&S.empty[stage]);
+                        // GG_FP8_ROWS: one commit per block; the epilogue, which it wakes, frees the stage
+                        if (!kRowsM) umma_commit_pair_both(&S.empty[stage]);
                         if (++stage == kGgStages) {
                             stage = 0;
                             phase ^= 1u;
@@ -756,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             }
             umma_commit_pair_self(&S.done);
             mbar_wait_bounded(&S.done, 0, 1u << 26, err);
-        } else if (warp >= 2 && OP == GG_FP8) {
+        } else if (warp >= 2 && kF8) {
             // -------------------------------------------- scale products
             const int tid = threadIdx.x - 64;
             const int kblocks = ceil_div(P.cdim, 128), fblocks = ceil_div(P.feat, 128);
@@ -766,41 +788,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
                 const GgTile ti = decode<OP>(P, S, t, e);
-                const int fb = ti.feat0 / 128 + (int)rank;
-                const float* sw = P.a_scale + ((long long)ti.e * fblocks + min(fb, fblocks - 1)) * kblocks;
+                // GG_FP8: this CTA's features are one weight block, entry c is row c of the tile.
+                // GG_FP8_ROWS: entry 128 h + r is this CTA's row r and weight block h of two.
+                const int fb = ti.feat0 / 128 + (kRowsM ? 0 : (int)rank);
+                const float* sw = P.a_scale + (long long)ti.e * fblocks * kblocks;
                 for (int kb0 = 0; kb0 < ti.nkb; kb0 += kScaleBatch) {
                     // all loads of the batch in flight at once, and under the wait
-                    float w[kScaleBatch];
-                    float4 v[kGgBN / 64];
+                    constexpr int kW = kRowsM ? 2 : 1, kR = kRowsM ? 2 : kGgBN / 64;
+                    float4 w[kW], v[kR];
 #pragma unroll
-                    for (int q = 0; q < kScaleBatch; ++q) w[q] = kb0 + q < kblocks ? __ldg(sw + kb0 + q) : 0.f;
+                    for (int i = 0; i < kW; ++i)
+                        w[i] = load_scales(sw + (long long)min(fb + i, fblocks - 1) * kblocks + kb0, kblocks - kb0, wide);
 #pragma unroll
-                    for (int i = 0; i < kGgBN / 64; ++i) {
-                        const int c = tid + 64 * i;
-                        const bool in = c < ti.ncols;
-                        const float* p = P.b_scale + (long long)(ti.row0 + (in ? c : 0)) * kblocks + kb0;
+                    for (int i = 0; i < kR; ++i) {
+                        const int c = tid + 64 * i, row = kRowsM ? (int)rank * 128 + c : c;
                         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (wide) {
-                            if (in) v[i] = __ldg(reinterpret_cast<const float4*>(p));
-                        } else {
-                            if (in) v[i].x = __ldg(p);
-                            if (in && kb0 + 1 < kblocks) v[i].y = __ldg(p + 1);
-                            if (in && kb0 + 2 < kblocks) v[i].z = __ldg(p + 2);
-                            if (in && kb0 + 3 < kblocks) v[i].w = __ldg(p + 3);
-                        }
+                        if (row < ti.ncols)
+                            v[i] = load_scales(P.b_scale + (long long)(ti.row0 + row) * kblocks + kb0, kblocks - kb0, wide);
                     }
                     if (!mbar_wait_bounded(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
                         ok = false;
                         break;
                     }
 #pragma unroll
-                    for (int i = 0; i < kGgBN / 64; ++i) {
+                    for (int i = 0; i < kR; ++i) {
                         const int c = tid + 64 * i;
-                        if (c < ti.neff) {
-                            S.scale[buf][0][c] = v[i].x * w[0];
-                            S.scale[buf][1][c] = v[i].y * w[1];
-                            S.scale[buf][2][c] = v[i].z * w[2];
-                            S.scale[buf][3][c] = v[i].w * w[3];
+                        if (kRowsM) {  // an entry's four blocks side by side: its thread reads them at once
+#pragma unroll
+                            for (int j = 0; j < kW; ++j)
+                                *reinterpret_cast<float4*>(&S.scale[buf][0][0] + 4 * (c + 128 * j)) =
+                                    make_float4(v[i].x * w[j].x, v[i].y * w[j].y, v[i].z * w[j].z, v[i].w * w[j].w);
+                        } else if (c < ti.neff) {
+#pragma unroll
+                            for (int j = 0; j < kW; ++j) {
+                                S.scale[buf][0][c + 128 * j] = v[i].x * w[j].x;
+                                S.scale[buf][1][c + 128 * j] = v[i].y * w[j].y;
+                                S.scale[buf][2][c + 128 * j] = v[i].z * w[j].z;
+                                S.scale[buf][3][c + 128 * j] = v[i].w * w[j].w;
+                            }
                         }
                     }
                     __syncwarp();
@@ -845,8 +870,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         // ------------------------------------------------ epilogue (both CTAs)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GgRegs<OP>::kEpi));
         const int q = warp & 3, h = (warp - 4) >> 2;
+        const uint32_t cempty0 = mapa_shared(&S.cempty[0], 0);
         if (kRowsM) {
-            epilogue_rows(P, S, pair, npairs, ntiles, rank, q, h, lane, tmem_base);
+            epilogue_rows(P, S, pair, npairs, ntiles, rank, q, h, lane, tmem_base, cempty0);
         } else {
         int buf = 0, sbuf = 0, e = 0;
         uint32_t bphase = 0, sphase = 0;
@@ -872,7 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                 uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * kGgBN + c0);
                 const float* sc = &S.scale[sbuf][kb0 % kScaleBatch][c0 + 2 * (lane & 3)];
                 const int parts = kF8 ? min(ck, ti.nkb - kb0) : 1;
-                const uint32_t release = mapa_shared(&S.cempty[buf], 0);
+                const uint32_t release = cempty0 + 8u * (uint32_t)buf;
                 for (int part = 0; part < parts; ++part) {
                     const bool last = part == parts - 1;
                     switch (ng) {

@@ -7,89 +7,79 @@ its tensors (ValueError), launches on the current stream of the tensors' device
 and raises ``LmoeError`` on a status from the library. Nothing synchronises, no
 workspace is kept, and the calls can be captured into a CUDA graph. None of them
 records an autograd graph: the gradients are calls of their own.
+
+The smallest calls take about as long to issue as to run, so the checks here
+touch each attribute once.
 """
 from __future__ import annotations
 
-import ctypes
+import torch
 
-_void = ctypes.c_void_p
+from . import LMOE_BF16, LMOE_FP32, LMOE_OK, LmoeError, load
+
+_BF16, _F32, _F8, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
+_CODE = {_BF16: LMOE_BF16, _F32: LMOE_FP32}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object
 
 
 def _fail(where, what):
     raise ValueError("%s: %s" % (where, what))
 
 
-def _rows(t, name, where, dtypes):
-    """Row pitch of a 2-D tensor whose columns are contiguous."""
-    if t.dim() != 2 or t.dtype not in dtypes:
-        _fail(where, "%s must be a 2-D tensor of %s, got %s %s" % (name, "/".join(map(str, dtypes)), tuple(t.shape), t.dtype))
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        _fail(where, "%s's columns must be contiguous (strides %s)" % (name, t.stride()))
+def _about(t):
+    return "%s %s on %s" % (tuple(t.shape), t.dtype, t.device) if isinstance(t, torch.Tensor) else repr(t)
+
+
+def _pitch(t, rows, cols, name, where):
+    """Row pitch of a 2-D tensor whose columns are contiguous and whose rows do not overlap."""
+    ld, step = t.stride()
     if rows <= 1:
-        return cols
-    ld = t.stride(0)
-    if ld < cols:
-        _fail(where, "%s's rows overlap (strides %s)" % (name, t.stride()))
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
+        _fail(where, "%s's columns must be contiguous and its rows must not overlap (strides %s)" % (name, t.stride()))
     return ld
 
 
-def _same_device(where, first, **others):
-    if not first.is_cuda:
-        _fail(where, "the tensors must be on a CUDA device")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            _fail(where, "%s is on %s, not on %s" % (name, t.device, first.device))
-
-
-def _counts(counts, groups, where):
-    import torch
-    if counts.dim() != 1 or counts.dtype != torch.int32 or counts.shape[0] != groups or not counts.is_contiguous():
-        _fail(where, "counts must be a contiguous int32 tensor [%d], got %s %s" % (groups, tuple(counts.shape), counts.dtype))
-
-
-def _out(out, shape, dtype, device, where):
-    """The output tensor, its row pitch and the library's type code."""
-    import torch
+def _out(where, out, dtype, x, shape):
+    """The output, its row pitch and the library's type code."""
     if out is None:
-        if dtype not in (torch.bfloat16, torch.float32):
+        dtype = dtype or _BF16
+        code = _CODE.get(dtype)
+        if code is None:
             _fail(where, "the output is bfloat16 or float32, not %s" % dtype)
-        out = torch.empty(shape, dtype=dtype, device=device)
-    else:
-        if tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
-            _fail(where, "out must be %s%s, got %s %s" % (tuple(shape), "" if dtype is None else " %s" % dtype,
-                                                         tuple(out.shape), out.dtype))
-        if out.device != device:
-            _fail(where, "out is on %s, not on %s" % (out.device, device))
+        return x.new_empty(shape, dtype=dtype), shape[-1], code
+    code = _CODE.get(out.dtype)
+    if code is None or out.shape != shape or (dtype is not None and out.dtype != dtype) or out.device != x.device:
+        _fail(where, "out must be %s%s on %s, got %s" % (shape, " %s" % dtype if dtype else " bfloat16 or float32", x.device,
+                                                        _about(out)))
     if len(shape) == 2:
-        ld = _rows(out, "out", where, (torch.bfloat16, torch.float32))
-    else:
-        if out.dtype not in (torch.bfloat16, torch.float32) or not out.is_contiguous():
-            _fail(where, "out must be a contiguous bfloat16 or float32 tensor")
-        ld = shape[-1]
-    return out, ld, 1 if out.dtype == torch.float32 else 0
+        return out, _pitch(out, shape[0], shape[1], "out", where), code
+    if not out.is_contiguous():
+        _fail(where, "out must be contiguous (strides %s)" % (out.stride(),))
+    return out, shape[-1], code
 
 
-def _call(name, device, *args):
-    """Launches lib.name(*args, stream) with `device` current."""
-    import torch
-    from . import LMOE_OK, LmoeError, load
-    fn = getattr(load(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        s = fn(*args, stream)
+def _launch(fn, index, *args):
+    """fn(*args, stream) with the tensors' device current, on its current stream."""
+    if torch.cuda.current_device() == index:
+        s = getattr(load(), fn)(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            s = fn(*args, stream)
+        with torch.cuda.device(index):
+            s = getattr(load(), fn)(*args, _raw_stream(index))
     if s != LMOE_OK:
-        raise LmoeError(s, name)
+        raise LmoeError(s, fn)
 
 
-def _weights(w, where):
-    import torch
-    if w.dim() != 3 or w.dtype != torch.bfloat16 or not w.is_contiguous():
-        _fail(where, "w must be a contiguous bfloat16 tensor [E, N, K], got %s %s" % (tuple(w.shape), w.dtype))
-    return w.shape
+def _is(t, dtype, dims, index):
+    return t.dtype is dtype and t.dim() == dims and t.get_device() == index
+
+
+def _explain(where, index, **tensors):
+    """Raises for the first tensor that is not as given by name=(tensor, dtype, dims)."""
+    for name, (t, dtype, dims) in tensors.items():
+        if not isinstance(t, torch.Tensor) or index < 0 or not _is(t, dtype, dims, index):
+            _fail(where, "%s must be a %d-D %s tensor on a CUDA device%s, got %s" %
+                  (name, dims, dtype, "" if index < 0 else " (%d)" % index, _about(t)))
 
 
 def grouped_gemm(x, w, counts, out=None, out_dtype=None, zero_tail=False):
@@ -97,56 +87,52 @@ def grouped_gemm(x, w, counts, out=None, out_dtype=None, zero_tail=False):
     counts [E] int32 rows per expert (on the device). Returns y [rows, N] in
     out_dtype (bfloat16 unless given, or out's). Rows behind the last expert's
     keep what they held; zero_tail writes zeros there."""
-    import torch
-    where = "grouped_gemm"
-    E, N, K = _weights(w, where)
-    _same_device(where, x, w=w, counts=counts)
-    ldx = _rows(x, "x", where, (torch.bfloat16,))
-    if x.shape[1] != K:
-        _fail(where, "x has %d columns, w %d" % (x.shape[1], K))
-    _counts(counts, E, where)
-    rows = x.shape[0]
-    y, ldy, code = _out(out, (rows, N), out_dtype or (torch.bfloat16 if out is None else None), x.device, where)
-    _call("latentmoe_grouped_gemm", x.device, x.data_ptr(), ldx, w.data_ptr(), counts.data_ptr(), E, rows, N, K,
-          y.data_ptr(), ldy, code, int(zero_tail))
+    index = x.get_device()
+    if index < 0 or not (_is(x, _BF16, 2, index) and _is(w, _BF16, 3, index) and _is(counts, _I32, 1, index)):
+        _explain("grouped_gemm", index, x=(x, _BF16, 2), w=(w, _BF16, 3), counts=(counts, _I32, 1))
+    rows, K = x.shape
+    E, N, Kw = w.shape
+    if Kw != K or counts.shape[0] != E or not w.is_contiguous() or not counts.is_contiguous():
+        _fail("grouped_gemm", "x [rows, K], w [E, N, K] and counts [E] must fit, w and counts contiguous: got %s, %s, %s" %
+              (_about(x), _about(w), _about(counts)))
+    y, ldy, code = _out("grouped_gemm", out, out_dtype, x, (rows, N))
+    _launch("latentmoe_grouped_gemm", index, x.data_ptr(), _pitch(x, rows, K, "x", "grouped_gemm"), w.data_ptr(),
+            counts.data_ptr(), E, rows, N, K, y.data_ptr(), ldy, code, zero_tail)
     return y
 
 
 def grouped_gemm_dx(dy, w, counts, out=None, out_dtype=None, zero_tail=False):
     """Gradient of grouped_gemm's input: dx[r] = dy[r] W[e(r)], dy [rows, N] bf16.
     Returns dx [rows, K]."""
-    import torch
-    where = "grouped_gemm_dx"
-    E, N, K = _weights(w, where)
-    _same_device(where, dy, w=w, counts=counts)
-    lddy = _rows(dy, "dy", where, (torch.bfloat16,))
-    if dy.shape[1] != N:
-        _fail(where, "dy has %d columns, w %d rows" % (dy.shape[1], N))
-    _counts(counts, E, where)
-    rows = dy.shape[0]
-    dx, lddx, code = _out(out, (rows, K), out_dtype or (torch.bfloat16 if out is None else None), dy.device, where)
-    _call("latentmoe_grouped_gemm_dx", dy.device, dy.data_ptr(), lddy, w.data_ptr(), counts.data_ptr(), E, rows, N, K,
-          dx.data_ptr(), lddx, code, int(zero_tail))
+    index = dy.get_device()
+    if index < 0 or not (_is(dy, _BF16, 2, index) and _is(w, _BF16, 3, index) and _is(counts, _I32, 1, index)):
+        _explain("grouped_gemm_dx", index, dy=(dy, _BF16, 2), w=(w, _BF16, 3), counts=(counts, _I32, 1))
+    rows, N = dy.shape
+    E, Nw, K = w.shape
+    if Nw != N or counts.shape[0] != E or not w.is_contiguous() or not counts.is_contiguous():
+        _fail("grouped_gemm_dx", "dy [rows, N], w [E, N, K] and counts [E] must fit, w and counts contiguous: got %s, %s, %s"
+              % (_about(dy), _about(w), _about(counts)))
+    dx, lddx, code = _out("grouped_gemm_dx", out, out_dtype, dy, (rows, K))
+    _launch("latentmoe_grouped_gemm_dx", index, dy.data_ptr(), _pitch(dy, rows, N, "dy", "grouped_gemm_dx"), w.data_ptr(),
+            counts.data_ptr(), E, rows, N, K, dx.data_ptr(), lddx, code, zero_tail)
     return dx
 
 
 def grouped_gemm_dw(dy, x, counts, out=None, out_dtype=None):
     """Gradient of grouped_gemm's weights: dW[e] = sum over expert e's rows of
     dy[r]^T x[r]. Returns dw [E, N, K]; an expert without rows gets zeros."""
-    import torch
-    where = "grouped_gemm_dw"
-    _same_device(where, dy, x=x, counts=counts)
-    lddy = _rows(dy, "dy", where, (torch.bfloat16,))
-    ldx = _rows(x, "x", where, (torch.bfloat16,))
+    index = dy.get_device()
+    if index < 0 or not (_is(dy, _BF16, 2, index) and _is(x, _BF16, 2, index) and _is(counts, _I32, 1, index)):
+        _explain("grouped_gemm_dw", index, dy=(dy, _BF16, 2), x=(x, _BF16, 2), counts=(counts, _I32, 1))
     rows, N = dy.shape
-    if x.shape[0] != rows:
-        _fail(where, "dy has %d rows, x %d" % (rows, x.shape[0]))
-    K = x.shape[1]
-    E = counts.shape[0] if counts.dim() == 1 else -1
-    _counts(counts, E, where)
-    dw, _, code = _out(out, (E, N, K), out_dtype or (torch.bfloat16 if out is None else None), dy.device, where)
-    _call("latentmoe_grouped_gemm_dw", dy.device, dy.data_ptr(), lddy, x.data_ptr(), ldx, counts.data_ptr(), E, rows, N, K,
-          dw.data_ptr(), code)
+    rows_x, K = x.shape
+    if rows_x != rows or not counts.is_contiguous():
+        _fail("grouped_gemm_dw", "dy [rows, N], x [rows, K] and contiguous counts [E] must fit: got %s, %s, %s" %
+              (_about(dy), _about(x), _about(counts)))
+    E = counts.shape[0]
+    dw, _, code = _out("grouped_gemm_dw", out, out_dtype, dy, (E, N, K))
+    _launch("latentmoe_grouped_gemm_dw", index, dy.data_ptr(), _pitch(dy, rows, N, "dy", "grouped_gemm_dw"), x.data_ptr(),
+            _pitch(x, rows, K, "x", "grouped_gemm_dw"), counts.data_ptr(), E, rows, N, K, dw.data_ptr(), code)
     return dw
 
 
@@ -154,25 +140,25 @@ def quantize_fp8(x, block_rows=1):
     """e4m3 codes and fp32 scales of x, bf16 or fp32: [R, K] or [n_mat, R, K] with one
     scale per block_rows x 128 elements. block_rows 1 (activations): scales
     [..., R, ceil(K/128)]; 128 (weights): scales [..., ceil(R/128), ceil(K/128)]."""
-    import torch
-    where = "quantize_fp8"
-    if block_rows not in (1, 128):
-        _fail(where, "block_rows is 1 or 128, not %r" % (block_rows,))
-    if x.dim() not in (2, 3) or x.dtype not in (torch.bfloat16, torch.float32):
-        _fail(where, "x must be a bfloat16 or float32 tensor [R, K] or [n_mat, R, K], got %s %s" % (tuple(x.shape), x.dtype))
-    _same_device(where, x)
-    n_mat = x.shape[0] if x.dim() == 3 else 1
-    R, K = x.shape[-2:]
-    if x.dim() == 3:
-        if not x.is_contiguous():
-            _fail(where, "x must be contiguous (strides %s)" % (x.stride(),))
-        ldx = K
+    index = x.get_device()
+    dims = x.dim()
+    code = _CODE.get(x.dtype)
+    if block_rows not in (1, 128) or dims not in (2, 3) or code is None or index < 0:
+        _fail("quantize_fp8", "x must be a bfloat16 or float32 tensor [R, K] or [n_mat, R, K] on a CUDA device and "
+              "block_rows 1 or 128: got %s, %r" % (_about(x), block_rows))
+    if dims == 2:
+        R, K = x.shape
+        n_mat, ldx = 1, _pitch(x, R, K, "x", "quantize_fp8")
+        scales = x.new_empty((-(-R // block_rows), -(-K // 128)), dtype=_F32)
     else:
-        ldx = _rows(x, "x", where, (torch.bfloat16, torch.float32))
-    codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    scales = torch.empty((*x.shape[:-2], -(-R // block_rows), -(-K // 128)), dtype=torch.float32, device=x.device)
-    _call("latentmoe_quantize_fp8", x.device, x.data_ptr(), ldx, 1 if x.dtype == torch.float32 else 0, n_mat, R, K,
-          block_rows, codes.data_ptr(), scales.data_ptr())
+        n_mat, R, K = x.shape
+        if not x.is_contiguous():
+            _fail("quantize_fp8", "a stack of matrices must be contiguous (strides %s)" % (x.stride(),))
+        ldx = K
+        scales = x.new_empty((n_mat, -(-R // block_rows), -(-K // 128)), dtype=_F32)
+    codes = x.new_empty(x.shape, dtype=_F8)
+    _launch("latentmoe_quantize_fp8", index, x.data_ptr(), ldx, code, n_mat, R, K, block_rows, codes.data_ptr(),
+            scales.data_ptr())
     return codes, scales
 
 
@@ -181,26 +167,28 @@ def gemm_fp8(xq, xs, wq, ws, counts=None, out=None, out_dtype=None, zero_tail=Fa
     with quantize_fp8's codes and scales: xq [rows, K], xs [rows, ceil(K/128)]. Without
     counts wq is [N, K] and ws [ceil(N/128), ceil(K/128)]; with counts [E] int32 the rows
     are in expert order, wq is [E, N, K] and ws [E, ceil(N/128), ceil(K/128)]."""
-    import torch
-    where = "gemm_fp8"
-    f8 = torch.float8_e4m3fn
-    lead = 0 if counts is None else 1
-    if wq.dim() != 2 + lead or wq.dtype != f8 or not wq.is_contiguous():
-        _fail(where, "wq must be a contiguous float8_e4m3fn tensor %s, got %s %s" %
-              ("[N, K]" if counts is None else "[E, N, K]", tuple(wq.shape), wq.dtype))
-    E = wq.shape[0] if lead else 1
-    N, K = wq.shape[-2:]
+    index = xq.get_device()
+    dims = 2 if counts is None else 3
+    if index < 0 or not (_is(xq, _F8, 2, index) and _is(xs, _F32, 2, index) and _is(wq, _F8, dims, index) and
+                         _is(ws, _F32, dims, index)):
+        _explain("gemm_fp8", index, xq=(xq, _F8, 2), xs=(xs, _F32, 2), wq=(wq, _F8, dims), ws=(ws, _F32, dims))
+    rows, K = xq.shape
     kb = -(-K // 128)
-    _same_device(where, xq, xs=xs, wq=wq, ws=ws, counts=counts)
-    if xq.dim() != 2 or xq.dtype != f8 or not xq.is_contiguous() or xq.shape[1] != K:
-        _fail(where, "xq must be a contiguous float8_e4m3fn tensor [rows, %d], got %s %s" % (K, tuple(xq.shape), xq.dtype))
-    rows = xq.shape[0]
-    for name, t, shape in (("xs", xs, (rows, kb)), ("ws", ws, (*wq.shape[:-2], -(-N // 128), kb))):
-        if tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous():
-            _fail(where, "%s must be a contiguous float32 tensor %s, got %s %s" % (name, tuple(shape), tuple(t.shape), t.dtype))
-    if counts is not None:
-        _counts(counts, E, where)
-    y, ldy, code = _out(out, (rows, N), out_dtype or (torch.bfloat16 if out is None else None), xq.device, where)
-    _call("latentmoe_gemm_fp8", xq.device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-          None if counts is None else counts.data_ptr(), E, rows, N, K, y.data_ptr(), ldy, code, int(zero_tail))
+    if counts is None:
+        E, ptr = 1, None
+        N, Kw = wq.shape
+        fit = ws.shape == (-(-N // 128), kb)
+    else:
+        if not _is(counts, _I32, 1, index):
+            _explain("gemm_fp8", index, counts=(counts, _I32, 1))
+        E, N, Kw = wq.shape
+        fit = ws.shape == (E, -(-N // 128), kb) and counts.shape[0] == E and counts.is_contiguous()
+        ptr = counts.data_ptr()
+    if not fit or Kw != K or xs.shape != (rows, kb) or not (
+            xq.is_contiguous() and xs.is_contiguous() and wq.is_contiguous() and ws.is_contiguous()):
+        _fail("gemm_fp8", "codes and scales must fit and be contiguous: got xq %s, xs %s, wq %s, ws %s, counts %s" %
+              (_about(xq), _about(xs), _about(wq), _about(ws), _about(counts)))
+    y, ldy, code = _out("gemm_fp8", out, out_dtype, xq, (rows, N))
+    _launch("latentmoe_gemm_fp8", index, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), ptr, E, rows, N, K,
+            y.data_ptr(), ldy, code, zero_tail)
     return y
