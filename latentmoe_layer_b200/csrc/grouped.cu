@@ -25,7 +25,7 @@
 //   warp 0       TMA producer (own 128 features of A, own half of B's rows)
 //   warp 1       TMEM owner; in the leader CTA, lane 0 issues the MMAs
 //   warps 2, 3   GG_FP8: the products sx * sw of the next four k-blocks, into
-//                shared memory; GG_DW: a group's last, partial k-block
+//                shared memory; GG_DW: zeros behind a group's last row
 //   warps 4-11   epilogue: drain TMEM chunks into fp32 registers, store
 // Tiles are found from prefix sums of the counts that every CTA builds in
 // shared memory, so a call is one launch and needs no workspace.
@@ -40,7 +40,7 @@
 //
 // A group's rows that do not fill a k-block of GG_DW (the contraction runs over
 // rows) must not meet the next group's, which may hold anything: warps 2 and 3
-// copy that k-block with plain loads and write zeros behind the last row.
+// write zeros over those rows of both operands once the k-block has landed.
 // Elsewhere rows of a neighbouring group land in output rows that are not
 // stored. Features and contraction indices past the matrix are zero-filled by
 // the tensor maps.
@@ -83,7 +83,7 @@ struct alignas(1024) GgShared {
     int tiles[kMaxE + 2];  // tile prefix per group
     long long wsum[kGgThreads / 32];
     uint64_t full[kGgStages], empty[kGgStages];
-    uint64_t tailreq[kGgStages], tail[kGgStages];  // GG_DW: stage handed to the copying warps, and back
+    uint64_t landed[kGgStages], tail[kGgStages];  // GG_DW: a partial k-block is in this CTA's stage; its end is zero
     uint64_t cfull[2], cempty[2], sfull[2], sempty[2], done;
     uint32_t tmem;
 };
@@ -205,6 +205,14 @@ __device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, i
     return ti;
 }
 
+// Load whose completion is counted in this CTA (bar: one of its own barriers).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t leader_bar, int x, int y,
                                                  int z) {
     asm volatile(
@@ -308,24 +316,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// GG_DW: 64 threads copy the last, partial k-block of one operand: 64
-// contraction rows (rows row .. row + rem of src, zeros behind) x `width`
-// columns from column c0, zeros past column `limit`. Sub-tiles of 64 columns,
-// 128-byte rows, 16-byte pieces swizzled by the row's index modulo 8. The copies
-// are asynchronous, all of them in flight at once (registers would hold a few).
-__device__ __forceinline__ void copy_partial(uint8_t* dst, const uint16_t* src, long long ld, int row, int rem, int c0,
-                                             int limit, int width, int tid) {
-    const uint32_t base = smem_u32(dst);
-    const int shift = width == 128 ? 4 : 3;  // 16-byte pieces per row: 16 or 8
-    for (int i = tid; i < 64 << shift; i += 64) {
-        const int r = i >> shift, q = i & ((1 << shift) - 1), c = c0 + q * 8;
-        const bool in = r < rem && c < limit;
-        const uint16_t* p = in ? src + (long long)(row + r) * ld + c : src;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         base + (uint32_t)((q >> 3) * 8192 + r * 128 + (((q & 7) ^ (r & 7)) << 4))),
-                     "l"(p), "r"(in ? 16 : 0)
-                     : "memory");
-    }
+// Zeros the rows from rem to the next multiple of 16 (the MMAs' depth; rows behind
+// that are not multiplied) of `subs` sub-tiles of 128-byte rows: 64 threads. Whole
+// rows, so the swizzle, which stays inside a row, does not matter.
+__device__ __forceinline__ void zero_rows(uint8_t* dst, int subs, int rem, int tid) {
+    const int end = ((rem + 15) & ~15) * 8;
+    for (int sub = 0; sub < subs; ++sub)
+        for (int i = rem * 8 + tid; i < end; i += 64)
+            *reinterpret_cast<uint4*>(dst + sub * 8192 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // 16 TMEM lanes x 32 columns: register 4 b + 2 s + j holds lane (l / 4) + 8 s, column
@@ -629,8 +627,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         for (int s = 0; s < kGgStages; ++s) {
             mbar_init(&S.full[s], 1);
             mbar_init(&S.empty[s], 1);
-            mbar_init(&S.tailreq[s], 1);
-            mbar_init(&S.tail[s], 4);  // two copying warps in each CTA
+            mbar_init(&S.landed[s], 1);
+            mbar_init(&S.tail[s], 4);  // two zeroing warps in each CTA
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&S.cfull[b], 1);
@@ -659,7 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         if (warp == 0 && elect_one()) {
             // -------------------------------------------- TMA producer (both CTAs)
             int stage = 0, e = 0;
-            uint32_t phase = 0, issued = 0, issued_par = 0;
+            uint32_t phase = 0, issued = 0, issued_par = 0, partial = 0, partial_n = 0;
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
                 const GgTile ti = decode<OP>(P, S, t, e);
@@ -672,10 +670,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                         break;
                     }
                     if (OP == GG_DW && ti.rem && kb == ti.nkb - 1) {
-                        // warps 2 and 3 fill this stage; its earlier load has been consumed
-                        mbar_arrive(&S.tailreq[stage]);
+                        // counted in this CTA, whose warps 2 and 3 then zero the rows behind the group
+                        const int r = ti.row0 + kb * 64;
+                        mbar_arrive_expect_tx(&S.landed[stage], kGgABytes + bytes_b);
+                        tma_load_3d(S.a[stage], &P.a_map, &S.landed[stage], f0, r, 0);
+                        tma_load_3d(S.a[stage] + 8192, &P.a_map, &S.landed[stage], f0 + 64, r, 0);
+                        tma_load_3d(S.b[stage], &P.b_map[0], &S.landed[stage], b0, r, 0);
+                        if (half > 64) tma_load_3d(S.b[stage] + 8192, &P.b_map[0], &S.landed[stage], b0 + 64, r, 0);
                         if (leader) mbar_arrive(&S.full[stage]);
-                        issued &= ~(1u << stage);
+                        issued &= ~(1u << stage);  // the stage's earlier load has been consumed
+                        partial |= 1u << stage;
+                        partial_n ^= 1u << stage;
                     } else {
                         if (leader) mbar_arrive_expect_tx(&S.full[stage], 2u * (kGgABytes + bytes_b));
                         const uint32_t bar = mapa_shared(&S.full[stage], 0);
@@ -716,6 +721,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             }
             // the leader's full barriers count both CTAs' bytes: waiting on them drains every
             // load of the pair before either CTA can pass the final cluster barrier
+            for (int s = 0; s < kGgStages; ++s)  // the stage's last partial block has parity (their number - 1) % 2
+                if ((partial >> s) & 1u) mbar_wait_bounded(&S.landed[s], (~partial_n >> s) & 1u, 1u << 26, err);
             if (leader)
                 for (int s = 0; s < kGgStages; ++s)
                     if ((issued >> s) & 1u) mbar_wait_bounded(&S.full[s], (issued_par >> s) & 1u, 1u << 26, err);
@@ -745,7 +752,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                             ok = false;
                             break;
                         }
+                        int steps = 4;
                         if (OP == GG_DW && ti.rem && kb == ti.nkb - 1) {
+                            steps = (ti.rem + 15) >> 4;
                             if (!mbar_wait_bounded_cluster(&S.tail[stage], (tphase >> stage) & 1u, P.spin, err)) {
                                 ok = false;
                                 break;
@@ -758,8 +767,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                         const uint64_t bd = kBMN ? sdesc_mn_sw128(sb) : sdesc_sw128(sb);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_pair<kF8>(d, ad + kk * a_step, bd + kk * b_step, idesc,
-                                           ((!kF8 && kb > kb0) || kk > 0) ? 1u : 0u);
+                            if (OP != GG_DW || kk < steps)
+                                umma_pair<kF8>(d, ad + kk * a_step, bd + kk * b_step, idesc,
+                                               ((!kF8 && kb > kb0) || kk > 0) ? 1u : 0u);
                         if (kF8) d += (uint32_t)ti.neff;
                         // GG_FP8_ROWS: one commit per block; the epilogue, which it wakes, frees the stage
                         if (!kRowsM) umma_commit_pair_both(&S.empty[stage]);
@@ -839,26 +849,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
         } else if (warp >= 2 && OP == GG_DW) {
             // -------------------------------------------- partial k-blocks
             const int tid = threadIdx.x - 64;
-            // These warps may be many rounds of the ring ahead of the loads, so a stage's own
-            // barriers say nothing to them: the producer hands the stage over.
             int stage = 0, e = 0;
-            uint32_t rphase = 0;
+            uint32_t lphase = 0;
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
                 const GgTile ti = decode<OP>(P, S, t, e);
                 if (ti.nkb == 0) continue;
                 stage = (stage + ti.nkb - 1) % kGgStages;  // of the tile's last k-block
                 if (ti.rem) {
-                    if (!mbar_wait_bounded(&S.tailreq[stage], (rphase >> stage) & 1u, P.spin, err)) {
+                    if (!mbar_wait_bounded(&S.landed[stage], (lphase >> stage) & 1u, P.spin, err)) {
                         ok = false;
                         break;
                     }
-                    rphase ^= 1u << stage;
-                    const int row = ti.row0 + (ti.nkb - 1) * 64, half = ti.neff / 2;
-                    copy_partial(S.a[stage], P.x, P.ldx, row, ti.rem, ti.feat0 + (int)rank * 128, P.feat, 128, tid);
-                    copy_partial(S.b[stage], P.dy, P.lddy, row, ti.rem, ti.col0 + (int)rank * half, P.cols,
-                                 (half + 63) & ~63, tid);
-                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    lphase ^= 1u << stage;
+                    zero_rows(S.a[stage], 2, ti.rem, tid);
+                    zero_rows(S.b[stage], ti.neff > 128 ? 2 : 1, ti.rem, tid);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(mapa_shared(&S.tail[stage], 0));

@@ -13,9 +13,6 @@ struct alignas(64) GgParams {
     const int* counts;    // [n_groups] rows per group; null: one group of n_rows rows
     const float* a_scale; // GG_FP8: [n_groups, ceil(feat / 128), ceil(cdim / 128)]
     const float* b_scale; // GG_FP8: [n_rows, ceil(cdim / 128)]
-    const uint16_t* x;    // GG_DW: the operands again, for the partial k-blocks
-    const uint16_t* dy;
-    long long ldx, lddy;
     void* out;
     long long ldo;        // output row pitch, elements
     int n_groups, n_rows;

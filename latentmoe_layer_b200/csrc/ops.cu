@@ -194,10 +194,6 @@ lmoe_status latentmoe_grouped_gemm_dw(const void* dy, long long lddy, const void
         return cuda_status(cudaMemsetAsync(dw, 0, (size_t)n_groups * N * K * (dw_dtype == LMOE_FP32 ? 4 : 2),
                                            static_cast<cudaStream_t>(stream)));
     GgParams P = base_params(*st, counts, n_groups, n_rows, dw_dtype);
-    P.x = static_cast<const uint16_t*>(x);
-    P.dy = static_cast<const uint16_t*>(dy);
-    P.ldx = ldx;
-    P.lddy = lddy;
     P.out = dw;
     P.ldo = K;
     P.feat = K;
