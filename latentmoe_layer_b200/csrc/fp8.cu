@@ -20,30 +20,53 @@
 namespace lmoe {
 namespace {
 
-__device__ __forceinline__ uint32_t max_bits(uint32_t m, float v) {
-    return max(m, __float_as_uint(v) & 0x7FFFFFFFu);
-}
-
-// Eight elements from p (16-byte aligned).
+// Eight elements as loaded: their values and the largest |x| pattern.
 template <bool kF32>
-__device__ __forceinline__ void load8(const void* p, float (&v)[8]) {
-    if (kF32) {
-        const uint4 a = ld_global_nc_v4(static_cast<const uint4*>(p)), b = ld_global_nc_v4(static_cast<const uint4*>(p) + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
-        const uint4 a = ld_global_nc_v4(static_cast<const uint4*>(p));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Eight {
+    uint4 w[kF32 ? 2 : 1];
+    __device__ __forceinline__ void zero() {
+        w[0] = make_uint4(0u, 0u, 0u, 0u);
+        if (kF32) w[kF32 ? 1 : 0] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void load(const void* p) {  // 16-byte aligned
+        w[0] = ld_global_nc_v4(static_cast<const uint4*>(p));
+        if (kF32) w[kF32 ? 1 : 0] = ld_global_nc_v4(static_cast<const uint4*>(p) + 1);
+    }
+    __device__ __forceinline__ uint32_t amax() const {
+        if (kF32) {
+            const uint32_t m = 0x7FFFFFFFu;
+            const uint4 a = w[0], b = w[kF32 ? 1 : 0];
+            return max(max(max(a.x & m, a.y & m), max(a.z & m, a.w & m)), max(max(b.x & m, b.y & m), max(b.z & m, b.w & m)));
+        }
+        const uint32_t m = 0x7FFF7FFFu;  // two bf16 patterns per word
+        const uint32_t q = __vmaxu2(__vmaxu2(w[0].x & m, w[0].y & m), __vmaxu2(w[0].z & m, w[0].w & m));
+        return max(q << 16, q & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t a[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            if (kF32) {
+                v[i] = __uint_as_float(a[i]);
+            } else {
+                v[2 * i] = __uint_as_float(a[i] << 16);
+                v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+            }
+        }
+        if (kF32) {
+            const uint4 b = w[kF32 ? 1 : 0];
+            v[4] = __uint_as_float(b.x);
+            v[5] = __uint_as_float(b.y);
+            v[6] = __uint_as_float(b.z);
+            v[7] = __uint_as_float(b.w);
         }
     }
-}
+};
 
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
+template <bool kF32>
+__device__ __forceinline__ uint2 encode8(const Eight<kF32>& x, float inv) {
+    float v[8];
+    x.values(v);
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -60,43 +83,37 @@ __device__ __forceinline__ float block_amax(uint32_t bits) {
     return __uint_as_float(max(bits, 0x0D800000u));  // 2^-100
 }
 
-// 1 x 128 blocks: 16 lanes per block, kUnroll blocks per half warp in flight.
-template <bool kF32>
-__global__ void __launch_bounds__(256) k_quantize_rows(const void* x, long long ldx, long long rows, int cols,
-                                                       uint8_t* codes, float* scales) {
-    constexpr int kUnroll = kF32 ? 2 : 4;
+// 1 x 128 blocks: 16 lanes per block; a half warp takes kU neighbouring blocks of one
+// row, all loads in flight at once.
+template <bool kF32, int kU>
+__global__ void __launch_bounds__(256) k_quantize_rows(const void* x, long long ldx, int rows, int cols, uint8_t* codes,
+                                                       float* scales) {
     const int kblocks = (cols + 127) / 128;
-    const long long total = rows * kblocks;
     const int sub = threadIdx.x & 15;
-    const long long first = (long long)(blockIdx.x * (blockDim.x / 16) + threadIdx.x / 16) * kUnroll;
-    float v[kUnroll][8];
-    uint32_t m[kUnroll];
-    long long row[kUnroll];
-    int col[kUnroll];
+    const int row = blockIdx.x * 16 + (threadIdx.x >> 4), kb0 = blockIdx.y * kU;
+    const int col0 = kb0 * 128 + sub * 8;
+    const bool in_rows = row < rows;
+    Eight<kF32> v[kU];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const long long b = first + u;
-        row[u] = b / kblocks;
-        col[u] = (int)(b - row[u] * kblocks) * 128 + sub * 8;
-        const bool in = b < total && col[u] < cols;
-        if (!in) col[u] = -1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-        if (in) load8<kF32>(static_cast<const char*>(x) + (row[u] * ldx + col[u]) * (kF32 ? 4 : 2), v[u]);
+    for (int u = 0; u < kU; ++u) {
+        v[u].zero();
+        if (in_rows && col0 + u * 128 < cols)
+            v[u].load(static_cast<const char*>(x) + (row * ldx + col0 + u * 128) * (kF32 ? 4 : 2));
     }
+    float mine = 0.f;  // lane u keeps block u's maximum
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        m[u] = 0u;
+    for (int u = 0; u < kU; ++u) {
+        uint32_t m = v[u].amax();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m[u] = max_bits(m[u], v[u][i]);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m[u] = max(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], o));
-        const float a = block_amax(m[u]);
-        if (col[u] >= 0) {
-            *reinterpret_cast<uint2*>(codes + row[u] * cols + col[u]) = encode8(v[u], __fdiv_rn(448.f, a));
-            if (sub == 0) scales[first + u] = __fdiv_rn(a, 448.f);
-        }
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float a = block_amax(m);
+        if (sub == u) mine = a;
+        if (in_rows && col0 + u * 128 < cols)
+            *reinterpret_cast<uint2*>(codes + (long long)row * cols + col0 + u * 128) =
+                encode8<kF32>(v[u], __fdiv_rn(448.f, a));
     }
+    if (in_rows && sub < kU && kb0 + sub < kblocks)
+        scales[(long long)row * kblocks + kb0 + sub] = __fdiv_rn(mine, 448.f);
 }
 
 // 128 x 128 blocks: one CTA of 512 threads per block, 4 pieces of 8 elements per thread.
@@ -107,20 +124,17 @@ __global__ void __launch_bounds__(512) k_quantize_blocks(const void* x, long lon
     const int kb = blockIdx.x, rb = blockIdx.y;
     const long long mat = blockIdx.z;
     const int col = kb * 128 + (threadIdx.x & 15) * 8;
-    float v[4][8];
+    Eight<kF32> v[4];
     uint32_t m = 0u;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int row = rb * 128 + u * 32 + (threadIdx.x >> 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
+        v[u].zero();
         if (row < rows && col < cols)
-            load8<kF32>(static_cast<const char*>(x) + ((mat * rows + row) * ldx + col) * (kF32 ? 4 : 2), v[u]);
+            v[u].load(static_cast<const char*>(x) + ((mat * rows + row) * ldx + col) * (kF32 ? 4 : 2));
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_bits(m, v[u][i]);
+    for (int u = 0; u < 4; ++u) m = max(m, v[u].amax());
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -131,9 +145,22 @@ __global__ void __launch_bounds__(512) k_quantize_blocks(const void* x, long lon
     for (int u = 0; u < 4; ++u) {
         const int row = rb * 128 + u * 32 + (threadIdx.x >> 4);
         if (row < rows && col < cols)
-            *reinterpret_cast<uint2*>(codes + (mat * rows + row) * cols + col) = encode8(v[u], inv);
+            *reinterpret_cast<uint2*>(codes + (mat * rows + row) * cols + col) = encode8<kF32>(v[u], inv);
     }
     if (threadIdx.x == 0) scales[(mat * gridDim.y + rb) * gridDim.x + kb] = __fdiv_rn(a, 448.f);
+}
+
+template <bool kF32>
+cudaError_t launch_rows(const void* x, long long ldx, int rows, int cols, uint8_t* codes, float* scales, cudaStream_t s) {
+    const int kblocks = (cols + 127) / 128;
+    const unsigned gx = (unsigned)((rows + 15) / 16);
+    // as many blocks per half warp as a row fills, unless that leaves SMs without work
+    // (64 rows of 8192: 6.1 us with four, 4.9 with one)
+    if (kblocks >= 4 && (long long)gx * ((kblocks + 3) / 4) >= 2 * tc_num_sms())
+        k_quantize_rows<kF32, 4><<<dim3(gx, (kblocks + 3) / 4), 256, 0, s>>>(x, ldx, rows, cols, codes, scales);
+    else
+        k_quantize_rows<kF32, 1><<<dim3(gx, kblocks), 256, 0, s>>>(x, ldx, rows, cols, codes, scales);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -142,12 +169,9 @@ cudaError_t launch_quantize_fp8(const void* x, bool f32, long long ldx, int n_ma
                                 uint8_t* codes, float* scales, cudaStream_t s) {
     const int kblocks = (cols + 127) / 128;
     if (block_rows == 1) {
-        const long long nrows = (long long)n_mat * rows;
-        const long long per = 16 * (f32 ? 2 : 4);  // blocks per CTA
-        const long long grid = (nrows * kblocks + per - 1) / per;
-        if (grid > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-        if (f32) k_quantize_rows<true><<<(unsigned)grid, 256, 0, s>>>(x, ldx, nrows, cols, codes, scales);
-        else k_quantize_rows<false><<<(unsigned)grid, 256, 0, s>>>(x, ldx, nrows, cols, codes, scales);
+        // the matrices' rows follow each other with the same pitch
+        return f32 ? launch_rows<true>(x, ldx, n_mat * rows, cols, codes, scales, s)
+                   : launch_rows<false>(x, ldx, n_mat * rows, cols, codes, scales, s);
     } else {
         const dim3 grid(kblocks, (rows + 127) / 128, n_mat);
         if (f32) k_quantize_blocks<true><<<grid, 512, 0, s>>>(x, ldx, rows, cols, codes, scales);

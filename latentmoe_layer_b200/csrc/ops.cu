@@ -93,7 +93,7 @@ bool encode_rows(const OpsState& st, GgParams& P, const void* base, bool bf16, i
     return true;
 }
 
-constexpr long long kMaxDim = 1LL << 24;        // N, K
+constexpr long long kMaxDim = 1LL << 22;        // N, K
 constexpr long long kMaxElems = 1LL << 38;      // elements of one operand
 constexpr long long kMaxTiles = 1LL << 30;      // tiles of one launch
 
