@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "liblatentmoe.so")
 SO_CHECKS = os.path.join(HERE, "liblatentmoe_checks.so")
 SOURCES = ["api.cu", "router.cu", "permute.cu", "gemm_tc.cu", "gemm_nvfp4.cu", "gemm_simt.cu", "nvfp4.cu", "zcheck.cu",
-           "ops.cu", "grouped.cu", "fp8.cu"]
+           "ops.cu", "grouped.cu", "few.cu", "fp8.cu"]
 HEADERS = ["lmoe_internal.h", "handle.h", "ptx.cuh", "gemm_common.cuh", "grouped.h"]
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-Xcompiler", "-fPIC",
          "-shared", "--expt-relaxed-constexpr", "-Xptxas", "-v"]

@@ -26,6 +26,10 @@ struct alignas(64) GgParams {
     unsigned spin;
 };
 
+// GG_FWD (f8 = false) and GG_FP8 for up to kFewRows rows, where the kernel that splits a matrix over
+// all SMs is the faster one (few.cu has both sides' times); P's tensor maps are not used.
+constexpr int kFewRows = 8;
+cudaError_t launch_few(bool f8, const void* w, const void* x, long long ldx_bytes, const GgParams& P, cudaStream_t s);
 cudaError_t launch_grouped(int op, const GgParams& P, cudaStream_t s);
 cudaError_t launch_quantize_fp8(const void* x, bool f32, long long ldx, int n_mat, int rows, int cols, int block_rows,
                                 uint8_t* codes, float* scales, cudaStream_t s);

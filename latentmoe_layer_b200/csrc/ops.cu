@@ -157,6 +157,8 @@ lmoe_status run_rows(bool dx, const void* a, long long lda, const void* w, const
     P.feat = out_cols;
     P.cdim = in_cols;
     P.zero_tail = zero_tail != 0;
+    if (!dx && n_rows <= kFewRows)
+        return cuda_status(launch_few(false, w, a, lda * 2, P, static_cast<cudaStream_t>(stream)));
     if (!encode(*st, &P.a_map, w, true, n_groups, N, K, K, dx ? 64 : 128) ||
         !encode_rows(*st, P, a, true, n_rows, in_cols, lda))
         return LMOE_ERR_CUDA;
@@ -238,6 +240,8 @@ lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, 
     P.feat = N;
     P.cdim = K;
     P.zero_tail = zero_tail != 0;
+    if (n_rows <= kFewRows)
+        return cuda_status(launch_few(true, wq, xq, K, P, static_cast<cudaStream_t>(stream)));
     if (!encode(*st, &P.a_map, wq, false, n_groups, N, K, K, 128) ||
         !encode_rows(*st, P, xq, false, n_rows, K, K))
         return LMOE_ERR_CUDA;

@@ -130,6 +130,7 @@ def check_product(y, xq, xs, wq, ws, counts):
 
 
 CASES = [
+    ([1] + [0] * 500 + [3, 0, 1], 40, 1040), ([0, 8], 136, 2048), ([9], 136, 2048), ([1] * 8, 72, 528), ([4, 0, 5], 264, 80),
     ([5], 8, 16), ([1], 128, 128), ([0, 0, 3, 0], 136, 64), ([31, 32, 33, 0, 1], 264, 144), ([64, 63, 65, 128], 520, 656),
     ([255, 256, 257], 256, 512), ([513, 0, 130, 700], 384, 1040), ([300], 2048, 2560), (spread(1031, 37, 1), 264, 464),
     (spread(40, 128, 2), 512, 512), (spread(333, 1024, 3, empty=0.7), 40, 48),
@@ -164,6 +165,20 @@ def test_rows_behind_the_last_group(zero_tail):
     lm.gemm_fp8(xq, xs, wq, ws, counts=c, out=y, zero_tail=zero_tail)
     check_product(y, xq, xs, wq, ws, counts)
     assert (y[357:] == (0.0 if zero_tail else -7.0)).all()
+
+
+@pytest.mark.parametrize("counts,rows", [([0, 1, 0], 8), ([0, 0], 5), ([2, 0, 3], 8)])
+def test_few_rows_and_a_tail(counts, rows):
+    N, K = 264, 528
+    xq, xs, wq, ws, c = operands(counts, N, K, rows=rows)
+    used = sum(counts)
+    xq.view(torch.uint8)[used:] = 0x7F
+    xs[used:] = float("nan")
+    for zero_tail in (False, True):
+        y = torch.full((rows, N), -7.0, device="cuda")
+        lm.gemm_fp8(xq, xs, wq, ws, counts=c, out=y, zero_tail=zero_tail)
+        check_product(y, xq, xs, wq, ws, counts)
+        assert (y[used:] == (0.0 if zero_tail else -7.0)).all()
 
 
 def test_bad_values_stay_in_their_rows():

@@ -72,7 +72,8 @@ def check_dw(dw, dy, x, counts):
 
 
 CASES = [
-    # counts, N, K
+    # counts, N, K; up to 8 rows take another kernel than more
+    ([1] + [0] * 500 + [3, 0, 1], 40, 1032), ([0, 8], 136, 2048), ([9], 136, 2048), ([1] * 8, 72, 520), ([4, 0, 5], 24, 72),
     ([5], 8, 8),
     ([1], 64, 64),
     ([0, 0, 3, 0], 128, 64),
@@ -163,6 +164,27 @@ def test_rows_behind_the_last_group(zero_tail):
         check_dw(dw, dy, x, counts)
         left = 0.0 if zero_tail else -7.0
         assert (y[used:] == left).all() and (dx[used:] == left).all()
+
+
+@pytest.mark.parametrize("counts,rows", [([0, 1, 0], 8), ([0, 0], 5), ([2, 0, 3], 8), ([1], 1), ([3], 7)])
+def test_few_rows_and_a_tail(counts, rows):
+    N, K = 136, 264
+    x, dy, w, c = make(counts, N, K, rows=rows)
+    used = sum(counts)
+    x[used:] = float("nan")
+    for dtype in (torch.bfloat16, torch.float32):
+        for zero_tail in (False, True):
+            y = torch.full((rows, N), -7.0, dtype=dtype, device="cuda")
+            lm.grouped_gemm(x, w, c, out=y, zero_tail=zero_tail)
+            check_forward(y, x, w, counts)
+            assert (y[used:] == (0.0 if zero_tail else -7.0)).all()
+    for over in ([5, 1 << 30, 7], [-1, 2, 1 << 30]):
+        c3 = torch.tensor(over, dtype=torch.int32, device="cuda")
+        w3 = torch.randn(3, N, K, device="cuda").bfloat16()
+        x3 = torch.randn(rows, K, device="cuda").bfloat16()
+        first = max(0, min(over[0], rows))
+        second = max(0, min(over[1], rows - first))
+        check_forward(lm.grouped_gemm(x3, w3, c3), x3, w3, [first, second, rows - first - second])
 
 
 def test_counts_that_do_not_fit():
