@@ -477,16 +477,29 @@ __device__ __forceinline__ void tmem_ld_32x16(uint32_t taddr, uint32_t* r) {
         : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-__device__ __forceinline__ void add_group(float* acc, const uint32_t* r, float s) {
+// Adds s x (32 lanes x 32 NG columns of TMEM) to acc and gives the buffer back when the
+// last load has arrived; loads run one group ahead of the additions.
+template <int NG>
+__device__ __forceinline__ void drain_rows(uint64_t (&acc)[64], uint32_t taddr, float s, uint32_t release, int lane) {
+    const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+    uint32_t raw[2][32];
+    tmem_ld_32x16(taddr, &raw[0][0]);
+    tmem_ld_32x16(taddr + 16, &raw[0][16]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = fmaf(__uint_as_float(r[i]), s, acc[i]);
+    for (int g = 0; g < NG; ++g) {
+        uint32_t* r = raw[g & 1];
+        tmem_ld_wait32(r);
+        if (g + 1 < NG) {
+            tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
+            tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1) + 16), &raw[(g + 1) & 1][16]);
+        } else {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_bare(release, lane == 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[16 * g + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), s2, acc[16 * g + i]);
+    }
 }
 
 // GG_FP8_ROWS: a warp holds 32 rows (a lane each) x 128 features of one weight
@@ -505,10 +518,9 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
     for (int t = pair; t < ntiles; t += npairs) {
         const GgTile ti = decode<GG_FP8_ROWS>(P, S, t, e);
         const int c0 = h * 128, hc = min(128, max(0, ti.neff - c0));  // the warp's columns
-        float acc[128];
+        uint64_t acc[64];  // columns 2 i and 2 i + 1
 #pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        uint32_t raw[2][16];
+        for (int i = 0; i < 64; ++i) acc[i] = 0ull;
         float4 f;
         for (int kb = 0; kb < ti.nkb; ++kb) {
             if (kb % kScaleBatch == 0) {
@@ -524,45 +536,16 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
             const float s = f.x;
             f = make_float4(f.y, f.z, f.w, 0.f);
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
-            if (hc == 128) {
-                // the next block's first loads run under this one's last additions
-                if (kb == 0) {
-                    if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
-                    free_stage();
-                    tc_fence_after();
-                    tmem_ld_32x16(taddr + (uint32_t)(buf * kGgBN), raw[0]);
-                }
-#pragma unroll
-                for (int g = 0; g < 7; ++g) {
-                    tmem_ld_wait16(raw[g & 1]);
-                    tmem_ld_32x16(taddr + (uint32_t)(buf * kGgBN + 16 * (g + 1)), raw[(g + 1) & 1]);
-                    add_group(acc + 16 * g, raw[g & 1], s);
-                }
-                tmem_ld_wait16(raw[1]);
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_bare(cempty0 + 8u * (uint32_t)buf, lane == 0);
-                if (kb + 1 < ti.nkb) {
-                    if (!mbar_wait_bounded(&S.cfull[buf ^ 1], bphase ^ (uint32_t)buf, P.spin, P.err)) return;
-                    free_stage();
-                    tc_fence_after();
-                    tmem_ld_32x16(taddr + (uint32_t)((buf ^ 1) * kGgBN), raw[0]);
-                }
-                add_group(acc + 112, raw[1], s);
-            } else {
-                if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
-                free_stage();
-                tc_fence_after();
-#pragma unroll
-                for (int g = 0; g < 6; ++g)
-                    if (16 * g < hc) {
-                        tmem_ld_32x16(taddr + (uint32_t)(buf * kGgBN + 16 * g), raw[0]);
-                        tmem_ld_wait16(raw[0]);
-                        add_group(acc + 16 * g, raw[0], s);
-                    }
-                tc_fence_before();
-                __syncwarp();
-                mbar_arrive_bare(cempty0 + 8u * (uint32_t)buf, lane == 0);
+            if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
+            free_stage();
+            tc_fence_after();
+            const uint32_t release = cempty0 + 8u * (uint32_t)buf, at = taddr + (uint32_t)(buf * kGgBN);
+            switch (hc) {
+                case 128: drain_rows<4>(acc, at, s, release, lane); break;
+                case 96: drain_rows<3>(acc, at, s, release, lane); break;
+                case 64: drain_rows<2>(acc, at, s, release, lane); break;
+                case 32: drain_rows<1>(acc, at, s, release, lane); break;
+                default: mbar_arrive_bare(release, lane == 0);
             }
             if (++buf == 2) {
                 buf = 0;
@@ -587,11 +570,16 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
                         for (int c = 0; c < 8; ++c) {
                             uint4 v;
                             if (P.out_f32) {
-                                const float* a = acc + 32 * g + 4 * c;
+                                float a[4];
+                                unpack2(acc[16 * g + 2 * c], a[0], a[1]);
+                                unpack2(acc[16 * g + 2 * c + 1], a[2], a[3]);
                                 v = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
                                                __float_as_uint(a[3]));
                             } else {
-                                const float* a = acc + 64 * (g & 1) + 8 * c;
+                                float a[8];
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    unpack2(acc[32 * (g & 1) + 4 * c + j], a[2 * j], a[2 * j + 1]);
                                 v = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
                                                pack_bf16x2(a[6], a[7]));
                             }
