@@ -258,8 +258,9 @@ lmoe_status latentmoe_update_bias(lmoe_handle* h, const int32_t* expert_counts, 
  *    as absent.
  *  - ldx, lddy, ...: row pitch in elements, at least the row's length, a multiple
  *    of 8. Weights are contiguous [n_groups, N, K]. 1 <= n_groups <= 1024;
- *    N a multiple of 8, K of 8 (fp8: 16), both at most 2^22, at most 2^38
- *    elements per operand (else LMOE_ERR_UNSUPPORTED). n_rows = 0 is allowed.
+ *    N a multiple of 8, K of 8 (fp8: 16), both at most 2^22, n_rows at most 2^30
+ *    (0 is allowed), at most 2^38 elements per operand (else
+ *    LMOE_ERR_UNSUPPORTED).
  *  - Outputs are bf16 (one rounding from fp32, nearest-even) or fp32. NaN and
  *    infinities stay in the rows (for dw: in the group) that they belong to.
  *  - An output must not overlap an input.

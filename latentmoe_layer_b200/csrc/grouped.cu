@@ -948,7 +948,7 @@ cudaError_t launch_op(const GgParams& P, int pairs, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;  // 0: set up at every launch
     if (!(ready.load(std::memory_order_acquire) & bit)) {
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, k_grouped<OP>);

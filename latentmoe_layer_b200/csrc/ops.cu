@@ -96,11 +96,13 @@ bool encode_rows(const OpsState& st, GgParams& P, const void* base, bool bf16, i
 constexpr long long kMaxDim = 1LL << 22;        // N, K
 constexpr long long kMaxElems = 1LL << 38;      // elements of one operand
 constexpr long long kMaxTiles = 1LL << 30;      // tiles of one launch
+constexpr int kMaxRows = 1 << 30;               // row indices and their tiles' ends stay inside 32 bits
 
 // Sizes of a product: n_rows rows in n_groups groups, weights [n_groups, N, K].
 lmoe_status check_sizes(int n_groups, int n_rows, int N, int K, int k_align) {
     if (n_groups <= 0 || n_rows < 0 || N <= 0 || K <= 0) return LMOE_ERR_INVALID_ARG;
-    if (n_groups > kMaxE || N % 8 || K % k_align || N > kMaxDim || K > kMaxDim) return LMOE_ERR_UNSUPPORTED;
+    if (n_groups > kMaxE || n_rows > kMaxRows || N % 8 || K % k_align || N > kMaxDim || K > kMaxDim)
+        return LMOE_ERR_UNSUPPORTED;
     if ((long long)n_groups * N > kMaxElems / K) return LMOE_ERR_UNSUPPORTED;
     const long long side = N > K ? N : K;
     if (((long long)n_rows / 256 + n_groups + 1) * ((side + 255) / 256) > kMaxTiles ||

@@ -59,8 +59,11 @@ def _out(where, out, dtype, x, shape):
     return out, shape[-1], code
 
 
-def _launch(fn, index, *args):
-    """fn(*args, stream) with the tensors' device current, on its current stream."""
+def _launch(fn, index, sizes, *args):
+    """fn(*args, stream) with the tensors' device current, on its current stream. `sizes`: the 32-bit ones among
+    the arguments, which ctypes would cut without a word."""
+    if max(sizes) > 0x7FFFFFFF:
+        _fail(fn, "a size is beyond 2^31 - 1: %s" % (sizes,))
     if torch.cuda.current_device() == index:
         s = getattr(load(), fn)(*args, _raw_stream(index))
     else:
@@ -96,7 +99,7 @@ def grouped_gemm(x, w, counts, out=None, out_dtype=None, zero_tail=False):
         _fail("grouped_gemm", "x [rows, K], w [E, N, K] and counts [E] must fit, w and counts contiguous: got %s, %s, %s" %
               (_about(x), _about(w), _about(counts)))
     y, ldy, code = _out("grouped_gemm", out, out_dtype, x, (rows, N))
-    _launch("latentmoe_grouped_gemm", index, x.data_ptr(), _pitch(x, rows, K, "x", "grouped_gemm"), w.data_ptr(),
+    _launch("latentmoe_grouped_gemm", index, (E, rows, N, K), x.data_ptr(), _pitch(x, rows, K, "x", "grouped_gemm"), w.data_ptr(),
             counts.data_ptr(), E, rows, N, K, y.data_ptr(), ldy, code, zero_tail)
     return y
 
@@ -113,7 +116,7 @@ def grouped_gemm_dx(dy, w, counts, out=None, out_dtype=None, zero_tail=False):
         _fail("grouped_gemm_dx", "dy [rows, N], w [E, N, K] and counts [E] must fit, w and counts contiguous: got %s, %s, %s"
               % (_about(dy), _about(w), _about(counts)))
     dx, lddx, code = _out("grouped_gemm_dx", out, out_dtype, dy, (rows, K))
-    _launch("latentmoe_grouped_gemm_dx", index, dy.data_ptr(), _pitch(dy, rows, N, "dy", "grouped_gemm_dx"), w.data_ptr(),
+    _launch("latentmoe_grouped_gemm_dx", index, (E, rows, N, K), dy.data_ptr(), _pitch(dy, rows, N, "dy", "grouped_gemm_dx"), w.data_ptr(),
             counts.data_ptr(), E, rows, N, K, dx.data_ptr(), lddx, code, zero_tail)
     return dx
 
@@ -131,7 +134,7 @@ def grouped_gemm_dw(dy, x, counts, out=None, out_dtype=None):
               (_about(dy), _about(x), _about(counts)))
     E = counts.shape[0]
     dw, _, code = _out("grouped_gemm_dw", out, out_dtype, dy, (E, N, K))
-    _launch("latentmoe_grouped_gemm_dw", index, dy.data_ptr(), _pitch(dy, rows, N, "dy", "grouped_gemm_dw"), x.data_ptr(),
+    _launch("latentmoe_grouped_gemm_dw", index, (E, rows, N, K), dy.data_ptr(), _pitch(dy, rows, N, "dy", "grouped_gemm_dw"), x.data_ptr(),
             _pitch(x, rows, K, "x", "grouped_gemm_dw"), counts.data_ptr(), E, rows, N, K, dw.data_ptr(), code)
     return dw
 
@@ -157,7 +160,7 @@ def quantize_fp8(x, block_rows=1):
         ldx = K
         scales = x.new_empty((n_mat, -(-R // block_rows), -(-K // 128)), dtype=_F32)
     codes = x.new_empty(x.shape, dtype=_F8)
-    _launch("latentmoe_quantize_fp8", index, x.data_ptr(), ldx, code, n_mat, R, K, block_rows, codes.data_ptr(),
+    _launch("latentmoe_quantize_fp8", index, (n_mat, R, K), x.data_ptr(), ldx, code, n_mat, R, K, block_rows, codes.data_ptr(),
             scales.data_ptr())
     return codes, scales
 
@@ -189,6 +192,6 @@ def gemm_fp8(xq, xs, wq, ws, counts=None, out=None, out_dtype=None, zero_tail=Fa
         _fail("gemm_fp8", "codes and scales must fit and be contiguous: got xq %s, xs %s, wq %s, ws %s, counts %s" %
               (_about(xq), _about(xs), _about(wq), _about(ws), _about(counts)))
     y, ldy, code = _out("gemm_fp8", out, out_dtype, xq, (rows, N))
-    _launch("latentmoe_gemm_fp8", index, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), ptr, E, rows, N, K,
+    _launch("latentmoe_gemm_fp8", index, (E, rows, N, K), xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), ptr, E, rows, N, K,
             y.data_ptr(), ldy, code, zero_tail)
     return y

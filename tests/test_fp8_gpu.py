@@ -235,3 +235,22 @@ def test_serving_an_expert_layer_in_8_bits():
     # x, up, a and down are each rounded to e4m3 (2^-4 at most, of the value): the square doubles the
     # first two, so at most 6 * 2^-4 of the terms' norm, the errors being independent of their signs
     assert float((y.float() - yb.float()).norm() / yb.float().norm()) < 6 * 2.0 ** -4
+
+
+def test_refusals_of_the_binding():
+    xq, xs, wq, ws, c = operands([3, 5], 136, 272)
+    bad = [lambda: lm.quantize_fp8(torch.zeros(4, 32, device="cuda").half()), lambda: lm.quantize_fp8(torch.zeros(32, device="cuda")),
+           lambda: lm.quantize_fp8(torch.zeros(4, 32, device="cuda"), block_rows=64),
+           lambda: lm.quantize_fp8(torch.zeros(32, 16, device="cuda").t()),
+           lambda: lm.quantize_fp8(torch.zeros(2, 8, 64, device="cuda")[:, :, :32]),
+           lambda: lm.gemm_fp8(xq, xs, wq, ws), lambda: lm.gemm_fp8(xq, xs, wq[0], ws[0], counts=c),
+           lambda: lm.gemm_fp8(xq, xs[:, :2], wq, ws, counts=c), lambda: lm.gemm_fp8(xq, xs, wq, ws[:, :1], counts=c),
+           lambda: lm.gemm_fp8(xq.view(torch.uint8), xs, wq, ws, counts=c), lambda: lm.gemm_fp8(xq, xs.double(), wq, ws, counts=c),
+           lambda: lm.gemm_fp8(xq, xs, wq, ws, counts=c[:1]), lambda: lm.gemm_fp8(xq, xs.cpu(), wq, ws, counts=c),
+           lambda: lm.gemm_fp8(xq[:, :256], xs, wq, ws, counts=c), lambda: lm.gemm_fp8(xq, xs, wq, ws, counts=c, out_dtype=torch.half)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(lm.LmoeError) as e:
+        lm.quantize_fp8(torch.zeros(4, 24, device="cuda"))
+    assert e.value.status == lm.LMOE_ERR_UNSUPPORTED

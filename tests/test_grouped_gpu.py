@@ -360,3 +360,88 @@ def test_expert_layer_trains():
     for got, ref in ((x.grad, ux.grad), (up.grad, uu.grad), (down.grad, ud.grad)):
         assert float((got.double() - ref).norm() / ref.norm()) < 10 * 2.0 ** -8
     assert not x.grad[used:].any() and not up.grad[1].any() and not down.grad[1].any()
+
+
+def test_refusals_of_the_binding():
+    x, dy, w, c = make([3, 5], 24, 40)
+    bad = [lambda: lm.grouped_gemm(x.float(), w, c), lambda: lm.grouped_gemm(x, w[0], c), lambda: lm.grouped_gemm(x, w, c.long()),
+           lambda: lm.grouped_gemm(x, w, c[:1]), lambda: lm.grouped_gemm(x, w.transpose(1, 2), c),
+           lambda: lm.grouped_gemm(x, w, c.cpu()), lambda: lm.grouped_gemm(x.cpu(), w, c), lambda: lm.grouped_gemm(dy, w, c),
+           lambda: lm.grouped_gemm(x.t(), w, c), lambda: lm.grouped_gemm(x[:1].expand(8, 40), w, c),
+           lambda: lm.grouped_gemm(x, w, c, out=torch.empty(8, 24, device="cuda").half()),
+           lambda: lm.grouped_gemm(x, w, c, out=torch.empty(7, 24, device="cuda")),
+           lambda: lm.grouped_gemm(x, w, c, out=torch.empty(24, 8, device="cuda").t()),
+           lambda: lm.grouped_gemm(x, w, c, out=torch.empty(8, 24, device="cuda"), out_dtype=torch.bfloat16),
+           lambda: lm.grouped_gemm(x, w, c, out_dtype=torch.float16), lambda: lm.grouped_gemm_dx(x, w, c),
+           lambda: lm.grouped_gemm_dw(dy, x[:4], c), lambda: lm.grouped_gemm_dw(dy, x, c.view(2, 1)),
+           lambda: lm.grouped_gemm_dw(dy, x, c, out=torch.empty(2, 40, 24, device="cuda").transpose(1, 2))]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    wide = torch.zeros(8, 48, device="cuda").bfloat16()
+    w42 = torch.zeros(2, 24, 42, device="cuda").bfloat16()
+    for call, status in ((lambda: lm.grouped_gemm(wide[:, 1:41], w, c), lm.LMOE_ERR_INVALID_ARG),  # rows not 16-byte aligned
+                         (lambda: lm.grouped_gemm(torch.zeros(8, 42, device="cuda").bfloat16(), w42, c), lm.LMOE_ERR_UNSUPPORTED)):
+        with pytest.raises(lm.LmoeError) as e:
+            call()
+        assert e.value.status == status
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, %r)
+import latentmoe_layer_b200 as lm
+x = torch.randn(40, 64, device="cuda").bfloat16()
+w = torch.randn(2, 72, 64, device="cuda").bfloat16()
+c = torch.tensor([15, 25], dtype=torch.int32, device="cuda")
+y, dw = torch.zeros(40, 72, device="cuda"), torch.zeros(2, 72, 64, device="cuda")
+dy = torch.randn(40, 72, device="cuda").bfloat16()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):   # the library's first calls in this process
+    lm.grouped_gemm(x, w, c, out=y)
+    lm.grouped_gemm_dw(dy, x, c, out=dw)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, lm.grouped_gemm(x, w, c, out_dtype=torch.float32)) and y.abs().sum() > 0
+assert torch.equal(dw, lm.grouped_gemm_dw(dy, x, c, out_dtype=torch.float32)) and dw.abs().sum() > 0
+print("captured first")
+"""
+
+
+def test_first_call_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST % root], stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout[-2000:]
+
+
+def test_two_threads_at_once():
+    """Calls from two host threads, each on a stream of its own."""
+    import threading
+    jobs = []
+    for seed in range(2):
+        counts = spread(700, 9, seed)
+        x, dy, w, c = make(counts, 264, 520, seed=seed)
+        jobs.append((counts, x, dy, w, c, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+
+    def work(job):
+        counts, x, dy, w, c, stream, got = job
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got.append((lm.grouped_gemm(x, w, c), lm.grouped_gemm_dw(dy, x, c, out_dtype=torch.float32)))
+
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for counts, x, dy, w, c, _, got in jobs:
+        assert len(got) == 20
+        check_forward(got[0][0], x, w, counts)
+        check_dw(got[0][1], dy, x, counts)
+        assert all(torch.equal(got[0][0], y) and torch.equal(got[0][1], dw) for y, dw in got)
