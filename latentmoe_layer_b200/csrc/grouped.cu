@@ -157,7 +157,8 @@ struct GgTile {
     int ncols;  // valid N-side rows of the tile
     int neff;   // the MMA's N: ncols rounded up to 32
     int feat0;  // first feature of the pair
-    int nkb;    // k-blocks
+    int kb0;    // first k-block of this pair's share of the contraction
+    int nkb;    // k-blocks of the share
     int rem;    // GG_DW: rows of the last k-block when it is partial, else 0
 };
 
@@ -165,7 +166,7 @@ struct GgTile {
 // features, so that the pairs running at once share both operands in L2.
 // `e` carries the last tile's group: a CTA's tiles only move forward.
 template <int OP>
-__device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, int t, int& e) {
+__device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, int t, int& e, int part, int splits) {
     if (t >= S.tiles[e + 1]) {
         int lo = e + 1, hi = P.n_groups;  // tiles[lo] <= t < tiles[hi + 1]
         while (lo < hi) {
@@ -192,13 +193,18 @@ __device__ __forceinline__ GgTile decode(const GgParams& P, const GgShared& S, i
         ti.row0 = S.off[e];
         ti.col0 = c * kGgBN;
         ti.ncols = min(kGgBN, P.cols - ti.col0);
+        ti.kb0 = 0;
         ti.nkb = ceil_div(cnt, 64);
         ti.rem = cnt & 63;
     } else {
         ti.row0 = S.off[e] + c * per;
         ti.col0 = 0;
         ti.ncols = min(per, cnt - c * per);
-        ti.nkb = e < P.n_groups ? ceil_div(P.cdim, OP == GG_FP8 || OP == GG_FP8_ROWS ? 128 : 64) : 0;
+        const int nkb = e < P.n_groups ? ceil_div(P.cdim, OP == GG_FP8 || OP == GG_FP8_ROWS ? 128 : 64) : 0;
+        constexpr int kUnit = OP == GG_FP8 ? kScaleBatch : 1;  // scales are read in batches
+        const int units = ceil_div(nkb, kUnit);
+        ti.kb0 = units * part / splits * kUnit;
+        ti.nkb = min(nkb, units * (part + 1) / splits * kUnit) - ti.kb0;
         ti.rem = 0;
     }
     ti.neff = ((OP == GG_FP8_ROWS ? min(kGgBN, P.feat - ti.feat0) : ti.ncols) + 31) & ~31;
@@ -238,6 +244,18 @@ __device__ __forceinline__ void umma_pair(uint32_t d, uint64_t a, uint64_t b, ui
             : "memory");
     else
         umma_bf16_pair(d, a, b, idesc, accumulate);
+}
+
+// Arrive on the barrier at this offset in both CTAs of the pair (bits of mask: their
+// ranks in the cluster) once the leader's tcgen05 operations so far have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t mask) {
+    asm volatile(
+        "{\n\t.reg .b16 m;\n\t"
+        "cvt.u16.u32 m, %1;\n\t"
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(mask)
+        : "memory");
 }
 
 // Operand whose contraction index runs along shared-memory rows (MN-major):
@@ -434,21 +452,31 @@ __device__ __forceinline__ void store_rows(const Acc& acc, uint8_t* stage, void*
 
 // Adds 32 lanes x 32 NG columns of TMEM to acc, GG_FP8 with a factor per column at sc (the
 // thread's first pair of columns); gives the buffer back after the last load of the
-// `last` part. Loads run one group ahead of the additions. (NG is a template argument
+// `last` part. bf16 loads run one group ahead of the additions. (NG is a template argument
 // because conditions between the groups cost moves of the registers in flight.)
 template <int NG, bool kF8>
 __device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const float* sc, bool last, uint32_t release,
                                               int lane) {
-    uint32_t raw[2][32];
-    tmem_ld_16x32(taddr, &raw[0][0]);
-    tmem_ld_16x32(taddr + (16u << 16), &raw[0][16]);
+    constexpr int kAhead = kF8 ? 0 : 1;  // GG_FP8's tiles mostly have one group, and its registers are full
+    uint32_t raw[1 + kAhead][32];
+    if (kAhead) {
+        tmem_ld_16x32(taddr, &raw[0][0]);
+        tmem_ld_16x32(taddr + (16u << 16), &raw[0][16]);
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        uint32_t* r = raw[g & 1];
+        uint32_t* r = raw[kAhead ? g & 1 : 0];
+        if (!kAhead) {
+            tmem_ld_16x32(taddr + (uint32_t)(32 * g), r);
+            tmem_ld_16x32(taddr + (uint32_t)(32 * g) + (16u << 16), r + 16);
+        }
         tmem_ld_wait32(r);
         if (g + 1 < NG) {
-            tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
-            tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)) + (16u << 16), &raw[(g + 1) & 1][16]);
+            if (kAhead) {
+                uint32_t* n = raw[kAhead ? (g + 1) & 1 : 0];
+                tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)), n);
+                tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)) + (16u << 16), n + 16);
+            }
         } else if (last) {
             tc_fence_before();
             __syncwarp();
@@ -506,17 +534,18 @@ __device__ __forceinline__ void drain_rows(uint64_t (&acc)[64], uint32_t taddr, 
 // block, so a 128-deep block's factor sx * sw is one register per thread and the
 // drain touches no shared memory, whose bandwidth the MMA's operands use up.
 __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, int pair, int npairs, int ntiles,
-                                              uint32_t rank, int q, int h, int lane, uint32_t tmem_base, uint32_t cempty0) {
+                                              uint32_t crank, int q, int h, int lane, uint32_t tmem_base, uint32_t cempty0) {
+    const uint32_t rank = crank & 1u;
     int buf = 0, sbuf = 0, e = 0, stage = 0;
     uint32_t bphase = 0, sphase = 0;
     const bool frees = q == 0 && h == 0 && lane == 0;
-    const uint32_t empty0 = mapa_shared(&S.empty[0], rank), sempty0 = mapa_shared(&S.sempty[0], rank);
+    const uint32_t empty0 = mapa_shared(&S.empty[0], crank), sempty0 = mapa_shared(&S.sempty[0], crank);
     auto free_stage = [&] {  // the block's operands have been read
         mbar_arrive_bare(empty0 + 8u * (uint32_t)stage, frees);
         if (++stage == kGgStages) stage = 0;
     };
     for (int t = pair; t < ntiles; t += npairs) {
-        const GgTile ti = decode<GG_FP8_ROWS>(P, S, t, e);
+        const GgTile ti = decode<GG_FP8_ROWS>(P, S, t, e, 0, 1);
         const int c0 = h * 128, hc = min(128, max(0, ti.neff - c0));  // the warp's columns
         uint64_t acc[64];  // columns 2 i and 2 i + 1
 #pragma unroll
@@ -601,16 +630,51 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
     }
 }
 
-template <int OP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant__ GgParams P) {
+// A split contraction: the pairs of a cluster each hold a tile's sum over their share.
+// The later ones write theirs into the stages of the first pair's CTA of the same
+// features (a[0] onwards: hc KB per pair), which adds them in order. Entry i of thread
+// t is at (i * 256 + t) * 8, so that a warp's accesses are contiguous.
+__device__ __forceinline__ void send_partial(const Acc& acc, uint8_t* stages, int part, uint32_t rank, int hc) {
+    const uint32_t to = mapa_shared(stages, rank) + (uint32_t)((part - 1) * hc * 1024 + ((int)threadIdx.x - 128) * 8);
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+        if (8 * b < hc) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(to + (uint32_t)((4 * b + i) * 2048)),
+                             "l"(acc[i >> 1][b][i & 1])
+                             : "memory");
+        }
+}
+__device__ __forceinline__ void add_partials(Acc& acc, const uint8_t* stages, int splits, int hc) {
+    for (int part = 1; part < splits; ++part) {
+        const uint8_t* from = stages + (part - 1) * hc * 1024 + ((int)threadIdx.x - 128) * 8;
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            if (8 * b < hc) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[i >> 1][b][i & 1] =
+                        add2(acc[i >> 1][b][i & 1], *reinterpret_cast<const uint64_t*>(from + (4 * b + i) * 2048));
+            }
+    }
+}
+
+// kSplit: a cluster holds P.splits pairs, which share each tile's contraction. (An
+// instantiation of its own: ranks known at compile time keep the others' registers
+// free of spills, which cost the 8-bit products 15%.)
+template <int OP, bool kSplit>
+__global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant__ GgParams P) {
     constexpr bool kF8 = OP == GG_FP8 || OP == GG_FP8_ROWS, kRowsM = OP == GG_FP8_ROWS, kAMN = OP == GG_DX || OP == GG_DW, kBMN = OP == GG_DW;
     extern __shared__ uint8_t smem_raw[];
     GgShared& S = *reinterpret_cast<GgShared*>(smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw)));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    // `pair` numbers the clusters
+    const uint32_t crank = cluster_ctarank(), rank = kSplit ? crank & 1u : crank, lead = kSplit ? crank & ~1u : 0u;
     const bool leader = rank == 0;
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int splits = kSplit ? P.splits : 1, part = kSplit ? (int)(crank >> 1) : 0;
+    const int pair = (int)blockIdx.x / (2 * splits), npairs = (int)gridDim.x / (2 * splits);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kGgStages; ++s) {
             mbar_init(&S.full[s], 1);
@@ -646,9 +710,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             // -------------------------------------------- TMA producer (both CTAs)
             int stage = 0, e = 0;
             uint32_t phase = 0, issued = 0, issued_par = 0, partial = 0, partial_n = 0;
+            const uint32_t full0 = mapa_shared(&S.full[0], lead);
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
-                const GgTile ti = decode<OP>(P, S, t, e);
+                const GgTile ti = decode<OP>(P, S, t, e, part, splits);
                 const int half = ti.neff / 2, f0 = ti.feat0 + (int)rank * 128;
                 const int b0 = (kBMN ? ti.col0 : ti.row0) + (int)rank * half;
                 const uint32_t bytes_b = kRowsM ? (uint32_t)kGgBBytes : kBMN ? (uint32_t)((half + 63) / 64) * 8192u : (uint32_t)half * 128u;
@@ -671,15 +736,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                         partial_n ^= 1u << stage;
                     } else {
                         if (leader) mbar_arrive_expect_tx(&S.full[stage], 2u * (kGgABytes + bytes_b));
-                        const uint32_t bar = mapa_shared(&S.full[stage], 0);
+                        const uint32_t bar = full0 + 8u * (uint32_t)stage;
                         if (kRowsM) {
                             tma_load_3d_pair(S.a[stage], &P.b_map[0], bar, kb * 128, ti.row0 + (int)rank * 128, 0);
                             tma_load_3d_pair(S.b[stage], &P.a_map, bar, kb * 128, ti.feat0 + (int)rank * half, ti.e);
                         } else if (OP == GG_FWD || OP == GG_FP8) {
-                            tma_load_3d_pair(S.a[stage], &P.a_map, bar, kb * (kF8 ? 128 : 64), f0, ti.e);
+                            tma_load_3d_pair(S.a[stage], &P.a_map, bar, (ti.kb0 + kb) * (kF8 ? 128 : 64), f0, ti.e);
                         } else if (OP == GG_DX) {
-                            tma_load_3d_pair(S.a[stage], &P.a_map, bar, f0, kb * 64, ti.e);
-                            tma_load_3d_pair(S.a[stage] + 8192, &P.a_map, bar, f0 + 64, kb * 64, ti.e);
+                            tma_load_3d_pair(S.a[stage], &P.a_map, bar, f0, (ti.kb0 + kb) * 64, ti.e);
+                            tma_load_3d_pair(S.a[stage] + 8192, &P.a_map, bar, f0 + 64, (ti.kb0 + kb) * 64, ti.e);
                         } else {
                             const int r = ti.row0 + kb * 64;
                             tma_load_3d_pair(S.a[stage], &P.a_map, bar, f0, r, 0);
@@ -688,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                             if (half > 64) tma_load_3d_pair(S.b[stage] + 8192, &P.b_map[0], bar, b0 + 64, r, 0);
                         }
                         if (!kBMN && !kRowsM) {
-                            const int x = kb * (kF8 ? 128 : 64);
+                            const int x = (ti.kb0 + kb) * (kF8 ? 128 : 64);
                             // half rows in boxes of 128, 64, 32 and 16: few requests, no row too many
                             int r = 0;
 #pragma unroll
@@ -724,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             uint32_t phase = 0, bphase = 0, tphase = 0;
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
-                const GgTile ti = decode<OP>(P, S, t, e);
+                const GgTile ti = decode<OP>(P, S, t, e, part, splits);
                 const uint32_t idesc = idesc0 | ((uint32_t)(ti.neff >> 3) << 17);
                 const int ck = kRowsM ? 1 : kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
                 for (int kb0 = 0; kb0 < ti.nkb && ok; kb0 += ck) {
@@ -760,14 +825,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                                                ((!kF8 && kb > kb0) || kk > 0) ? 1u : 0u);
                         if (kF8) d += (uint32_t)ti.neff;
                         // GG_FP8_ROWS: one commit per block; the epilogue, which it wakes, frees the stage
-                        if (!kRowsM) umma_commit_pair_both(&S.empty[stage]);
+                        if (!kRowsM) commit_pair(&S.empty[stage], 3u << lead);
                         if (++stage == kGgStages) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    umma_commit_pair_both(&S.cfull[buf]);
+                    commit_pair(&S.cfull[buf], 3u << lead);
                     if (++buf == 2) {
                         buf = 0;
                         bphase ^= 1u;
@@ -785,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             uint32_t bphase = 0;
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
-                const GgTile ti = decode<OP>(P, S, t, e);
+                const GgTile ti = decode<OP>(P, S, t, e, part, splits);
                 // GG_FP8: this CTA's features are one weight block, entry c is row c of the tile.
                 // GG_FP8_ROWS: entry 128 h + r is this CTA's row r and weight block h of two.
                 const int fb = ti.feat0 / 128 + (kRowsM ? 0 : (int)rank);
@@ -796,13 +861,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                     float4 w[kW], v[kR];
 #pragma unroll
                     for (int i = 0; i < kW; ++i)
-                        w[i] = load_scales(sw + (long long)min(fb + i, fblocks - 1) * kblocks + kb0, kblocks - kb0, wide);
+                        w[i] = load_scales(sw + (long long)min(fb + i, fblocks - 1) * kblocks + ti.kb0 + kb0, kblocks - ti.kb0 - kb0, wide);
 #pragma unroll
                     for (int i = 0; i < kR; ++i) {
                         const int c = tid + 64 * i, row = kRowsM ? (int)rank * 128 + c : c;
                         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (row < ti.ncols)
-                            v[i] = load_scales(P.b_scale + (long long)(ti.row0 + row) * kblocks + kb0, kblocks - kb0, wide);
+                            v[i] = load_scales(P.b_scale + (long long)(ti.row0 + row) * kblocks + ti.kb0 + kb0, kblocks - ti.kb0 - kb0,
+                                               wide);
                     }
                     if (!mbar_wait_bounded(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
                         ok = false;
@@ -841,7 +907,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
             uint32_t lphase = 0;
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
-                const GgTile ti = decode<OP>(P, S, t, e);
+                const GgTile ti = decode<OP>(P, S, t, e, part, splits);
                 if (ti.nkb == 0) continue;
                 stage = (stage + ti.nkb - 1) % kGgStages;  // of the tile's last k-block
                 if (ti.rem) {
@@ -857,25 +923,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                     // the fence above hands the zeros to the MMA; a cluster-scope release on top of it
                     // costs 7% of a training batch's weight gradient
                     if (lane == 0)
-                        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(&S.tail[stage], 0))
+                        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(&S.tail[stage], lead))
                                      : "memory");
                 }
                 if (++stage == kGgStages) stage = 0;
             }
         }
+        if (kSplit && pair < ntiles) {  // the epilogue's exchange of partial sums
+            __syncwarp();
+            cluster_sync_all();
+            cluster_sync_all();
+        }
     } else {
         // ------------------------------------------------ epilogue (both CTAs)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(GgRegs<OP>::kEpi));
         const int q = warp & 3, h = (warp - 4) >> 2;
-        const uint32_t cempty0 = mapa_shared(&S.cempty[0], 0);
+        const uint32_t cempty0 = mapa_shared(&S.cempty[0], lead);
         if (kRowsM) {
-            epilogue_rows(P, S, pair, npairs, ntiles, rank, q, h, lane, tmem_base, cempty0);
+            epilogue_rows(P, S, pair, npairs, ntiles, crank, q, h, lane, tmem_base, cempty0);
         } else {
         int buf = 0, sbuf = 0, e = 0;
         uint32_t bphase = 0, sphase = 0;
         bool ok = true;
         for (int t = pair; t < ntiles && ok; t += npairs) {
-            const GgTile ti = decode<OP>(P, S, t, e);
+            const GgTile ti = decode<OP>(P, S, t, e, part, splits);
             const int hc = ti.neff / 2, c0 = h * hc;  // this warp's accumulator columns c0 .. c0 + hc
             Acc acc;
 #pragma unroll
@@ -922,7 +993,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
                     }
                 }
             }
-            if (!ok) break;
+            if (kSplit) {
+                cluster_sync_all();  // every pair's operands are read, so the first pair's stages are free
+                if (ok && part > 0) send_partial(acc, S.a[0], part, rank, hc);
+                cluster_sync_all();
+                if (ok && part == 0) add_partials(acc, S.a[0], splits, hc);
+            }
+            if (!ok || part > 0) break;
             const int f = ti.feat0 + (int)rank * 128 + q * 32;
             const int nv = min(hc, ti.ncols - c0);
             const long long first = OP == GG_DW ? (long long)ti.e * P.cols + ti.col0 + c0 : (long long)ti.row0 + c0;
@@ -942,8 +1019,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1) k_gro
 // Sets the kernel's shared memory once per device and checks the register
 // split: setmaxnreg.inc would wait for ever if the launch brought fewer
 // registers than kLaunchRegs per thread.
-template <int OP>
-cudaError_t launch_op(const GgParams& P, int pairs, cudaStream_t s) {
+template <int OP, bool kSplit>
+cudaError_t launch_op(const GgParams& P, int clusters, cudaStream_t s) {
     static std::atomic<unsigned long long> ready{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -951,33 +1028,63 @@ cudaError_t launch_op(const GgParams& P, int pairs, cudaStream_t s) {
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;  // 0: set up at every launch
     if (!(ready.load(std::memory_order_acquire) & bit)) {
         cudaFuncAttributes fa;
-        e = cudaFuncGetAttributes(&fa, k_grouped<OP>);
+        e = cudaFuncGetAttributes(&fa, k_grouped<OP, kSplit>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidKernelImage;
-        e = cudaFuncSetAttribute(k_grouped<OP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGgSmem);
+        e = cudaFuncSetAttribute(k_grouped<OP, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGgSmem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    k_grouped<OP><<<2 * pairs, kGgThreads, kGgSmem, s>>>(P);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * P.splits * clusters);
+    cfg.blockDim = dim3(kGgThreads);
+    cfg.dynamicSmemBytes = kGgSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * P.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_grouped<OP, kSplit>, P);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_grouped(int op, const GgParams& P, cudaStream_t s) {
-    // no more pairs than tiles: an upper bound, the counts are on the device
+cudaError_t launch_grouped(int op, const GgParams& params, cudaStream_t s) {
+    GgParams P = params;
+    // tiles, as an upper bound: the counts are on the device
     const long long ft = (P.feat + 255) / 256;
-    const long long ct = op == GG_DW ? (long long)P.n_groups * ((P.cols + kGgBN - 1) / kGgBN)
-                                     : (long long)P.n_rows / kGgBN + P.n_groups + (P.zero_tail ? 1 : 0);
-    long long pairs = tc_num_sms() / 2;
-    if (ft * ct < pairs) pairs = ft * ct;
-    if (pairs < 1) return cudaSuccess;
+    const int groups = P.n_groups < P.n_rows ? P.n_groups : P.n_rows;
+    const long long tiles = op == GG_DW ? ft * P.n_groups * ((P.cols + kGgBN - 1) / kGgBN)
+                            : P.counts ? ft * (P.n_rows / kGgBN + groups + (P.zero_tail ? 1 : 0))
+                                       : ft * ((P.n_rows + kGgBN - 1) / kGgBN);
+    const int pairs = tc_num_sms() / 2;
+    // Few tiles and a long contraction (32 k-blocks or more): the pairs of a cluster share it. Four
+    // pairs where the exchange has room (128 rows) and all clusters of eight SMs run at once (about
+    // a dozen do), else two. One group of 32 rows, 1024 x 8192: 32.8 -> 17.3 us (8-bit 25.3 -> 16.0);
+    // eight groups of 4, 512 x 4096: 20.5 -> 16.5. At 16 k-blocks it costs more than it gains (8192 x
+    // 1024, 100 rows: 12.3 against 14.5). 8-bit rows on M past 128 rows gain nothing and stay.
+    P.splits = 1;
+    if (op != GG_DW && P.cdim > 31 * (op < GG_FP8 ? 64 : 128)) {
+        if (tiles <= 8 && P.n_rows <= 128) {
+            P.splits = 4;
+            if (op == GG_FP8_ROWS) op = GG_FP8;
+        } else if (tiles <= 32 && op != GG_FP8_ROWS) {
+            P.splits = 2;
+        }
+    }
+    long long clusters = pairs;
+    if (tiles < clusters || P.splits > 1) clusters = tiles;
+    if (clusters < 1) return cudaSuccess;
     switch (op) {
-        case GG_FWD: return launch_op<GG_FWD>(P, (int)pairs, s);
-        case GG_DX: return launch_op<GG_DX>(P, (int)pairs, s);
-        case GG_DW: return launch_op<GG_DW>(P, (int)pairs, s);
-        case GG_FP8: return launch_op<GG_FP8>(P, (int)pairs, s);
-        case GG_FP8_ROWS: return launch_op<GG_FP8_ROWS>(P, (int)pairs, s);
+        case GG_FWD: return P.splits > 1 ? launch_op<GG_FWD, true>(P, (int)clusters, s) : launch_op<GG_FWD, false>(P, (int)clusters, s);
+        case GG_DX: return P.splits > 1 ? launch_op<GG_DX, true>(P, (int)clusters, s) : launch_op<GG_DX, false>(P, (int)clusters, s);
+        case GG_FP8: return P.splits > 1 ? launch_op<GG_FP8, true>(P, (int)clusters, s) : launch_op<GG_FP8, false>(P, (int)clusters, s);
+        case GG_DW: return launch_op<GG_DW, false>(P, (int)clusters, s);
+        case GG_FP8_ROWS: return launch_op<GG_FP8_ROWS, false>(P, (int)clusters, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -21,7 +21,8 @@ struct alignas(64) GgParams {
     int cols;             // GG_DW: rows of each dW[e]
     int out_f32;
     int zero_tail;        // 1: rows behind the last group are written as zeros
-    int chunk_kb;         // k-blocks per TMEM chunk (GG_FP8: always 1)
+    int chunk_kb;         // k-blocks per TMEM chunk (8-bit: set by the tile)
+    int splits;           // set by launch_grouped: pairs (a cluster of them) that share a tile's contraction
     int* err;
     unsigned spin;
 };

@@ -134,6 +134,7 @@ CASES = [
     ([5], 8, 16), ([1], 128, 128), ([0, 0, 3, 0], 136, 64), ([31, 32, 33, 0, 1], 264, 144), ([64, 63, 65, 128], 520, 656),
     ([255, 256, 257], 256, 512), ([513, 0, 130, 700], 384, 1040), ([300], 2048, 2560), (spread(1031, 37, 1), 264, 464),
     (spread(40, 128, 2), 512, 512), (spread(333, 1024, 3, empty=0.7), 40, 48),
+    ([40], 264, 4096), ([20, 0, 30], 136, 4112), ([100], 520, 4096), ([60, 61, 0, 62], 520, 4368),  # shared contractions
 ]
 
 
@@ -157,14 +158,15 @@ def test_dense_product(rows, N, K, dtype):
 
 @pytest.mark.parametrize("zero_tail", [False, True])
 def test_rows_behind_the_last_group(zero_tail):
-    counts, rows, N, K = [40, 0, 300, 17], 700, 136, 272
-    xq, xs, wq, ws, c = operands(counts, N, K, rows=rows)
-    xq.view(torch.uint8)[357:] = 0x7F  # NaN codes and scales in rows that nobody may read into a result
-    xs[357:] = float("nan")
-    y = torch.full((rows, N), -7.0, device="cuda").bfloat16()
-    lm.gemm_fp8(xq, xs, wq, ws, counts=c, out=y, zero_tail=zero_tail)
-    check_product(y, xq, xs, wq, ws, counts)
-    assert (y[357:] == (0.0 if zero_tail else -7.0)).all()
+    for counts, rows, N, K in (([40, 0, 300, 17], 700, 136, 272), ([20, 0, 9], 60, 264, 4112), ([100, 900], 1400, 264, 272)):
+        used = sum(counts)
+        xq, xs, wq, ws, c = operands(counts, N, K, rows=rows)
+        xq.view(torch.uint8)[used:] = 0x7F  # NaN codes and scales in rows that nobody may read into a result
+        xs[used:] = float("nan")
+        y = torch.full((rows, N), -7.0, device="cuda").bfloat16()
+        lm.gemm_fp8(xq, xs, wq, ws, counts=c, out=y, zero_tail=zero_tail)
+        check_product(y, xq, xs, wq, ws, counts)
+        assert (y[used:] == (0.0 if zero_tail else -7.0)).all()
 
 
 @pytest.mark.parametrize("counts,rows", [([0, 1, 0], 8), ([0, 0], 5), ([2, 0, 3], 8)])

@@ -88,6 +88,8 @@ CASES = [
     (spread(333, 1024, 3, empty=0.7), 40, 48),
     ([2999, 0, 64 * 40, 64 * 13 + 1, 7, 1600 - 3], 1288, 776),  # many k-blocks between partial ones
     (spread(9000, 24, 4), 520, 264),
+    # few tiles and a long contraction (for dx: N): shared by two or four pairs of SMs
+    ([40], 264, 4096), ([20, 0, 30], 136, 2952), ([200], 520, 2056), ([100, 28], 4104, 72), ([0, 300], 2568, 520), ([90], 72, 456),
 ]
 IDS = ["%dx%d e%d r%d" % (n, k, len(c), sum(c)) for c, n, k in CASES]
 
@@ -148,7 +150,12 @@ def test_gradients_against_differences():
 @pytest.mark.parametrize("zero_tail", [False, True])
 def test_rows_behind_the_last_group(zero_tail):
     """Rows behind the last group may hold NaN: nobody reads them, and their outputs stay or become zero."""
-    counts, rows, N, K = [40, 0, 300, 17], 700, 136, 264
+    check_tail([40, 0, 300, 17], 700, 136, 264, zero_tail)
+    check_tail([20, 0, 9], 60, 2568, 2056, zero_tail)  # contraction shared by four pairs
+    check_tail([0, 0], 40, 136, 2056, zero_tail)
+
+
+def check_tail(counts, rows, N, K, zero_tail):
     x, dy, w, c = make(counts, N, K, rows=rows)
     used = sum(counts)
     x[used:] = float("nan")
