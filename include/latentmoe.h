@@ -292,7 +292,7 @@ lmoe_status latentmoe_grouped_gemm_dw(const void* dy, long long lddy, const void
  *   code = nearest e4m3 to x * (448 / a), saturating at 448
  * The element's value is code * scale. A NaN makes its block NaN (codes and
  * scale); an infinity makes its block's scale infinite. K a multiple of 16, ldx
- * of 8 (fp32: 4), at most 2^31 - 1 row blocks. */
+ * of 8 (fp32: 4), at most 2^31 - 16 blocks of one row. */
 lmoe_status latentmoe_quantize_fp8(const void* x, long long ldx, lmoe_dtype x_dtype, int n_mat, int R, int K,
                                    int block_rows, void* codes, float* scales, void* stream);
 /* The product of quantised operands, with nb = ceil(K / 128):

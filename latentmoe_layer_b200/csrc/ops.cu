@@ -97,6 +97,7 @@ constexpr long long kMaxDim = 1LL << 22;        // N, K
 constexpr long long kMaxElems = 1LL << 38;      // elements of one operand
 constexpr long long kMaxTiles = 1LL << 30;      // tiles of one launch
 constexpr int kMaxRows = 1 << 30;               // row indices and their tiles' ends stay inside 32 bits
+constexpr long long kMaxRowBlocks = 0x7FFFFFF0; // of the quantiser: rows rounded up to its 16 per CTA stay inside 32 bits
 
 // Sizes of a product: n_rows rows in n_groups groups, weights [n_groups, N, K].
 lmoe_status check_sizes(int n_groups, int n_rows, int N, int K, int k_align) {
@@ -217,7 +218,7 @@ lmoe_status latentmoe_quantize_fp8(const void* x, long long ldx, lmoe_dtype x_dt
     if (ldx % (x_dtype == LMOE_FP32 ? 4 : 8)) return LMOE_ERR_INVALID_ARG;
     if (K % 16 || K > kMaxDim || n_mat > 65535 || (block_rows == 128 && R > 65535 * 128)) return LMOE_ERR_UNSUPPORTED;
     const long long rows = (long long)n_mat * R;
-    if (ldx > kMaxElems / rows || rows * ((K + 127) / 128) > 0x7FFFFFFFLL) return LMOE_ERR_UNSUPPORTED;
+    if (ldx > kMaxElems / rows || rows * ((K + 127) / 128) > kMaxRowBlocks) return LMOE_ERR_UNSUPPORTED;
     return cuda_status(launch_quantize_fp8(x, x_dtype == LMOE_FP32, ldx, n_mat, R, K, block_rows,
                                            static_cast<uint8_t*>(codes), scales, static_cast<cudaStream_t>(stream)));
 }

@@ -67,6 +67,7 @@ def test_weight_gradient_refusals(lib, kw, status):
     (dict(codes=A + 8), INVALID), (dict(scales=A + 2), INVALID), (dict(ldx=128), INVALID), (dict(ldx=260), INVALID),
     (dict(K=264, ldx=264), UNSUPPORTED), (dict(n_mat=65536), UNSUPPORTED), (dict(K=1 << 23, ldx=1 << 23), UNSUPPORTED),
     (dict(n_mat=65535, R=1 << 20), UNSUPPORTED), (dict(R=65536 * 128, block=128), UNSUPPORTED),
+    (dict(R=2 ** 31 - 15, K=16, ldx=16), UNSUPPORTED),  # the last CTA's rows would pass 32 bits
 ])
 def test_quantiser_refusals(lib, kw, status):
     a = dict(x=A, ldx=256, dtype=0, n_mat=1, R=64, K=256, block=1, codes=A, scales=A)
