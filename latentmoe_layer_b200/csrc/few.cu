@@ -6,12 +6,15 @@
 // Bound by reading each hit expert's weights once. The tcgen05 engine gives a
 // 256-feature tile to a pair of SMs and keeps the tile's whole contraction there:
 // a 1024 x 8192 matrix is 4 tiles, for 74 pairs. Here a CTA takes 16 features, its
-// eight warps share the contraction and add up in shared memory, so every SM
-// streams (3 CTAs of 256 threads each, 16-byte loads, the next step's in flight
-// under this one's products). Device time by events (about 4 us of it the events'),
-// one row, 8-bit weights: 2560 x 2048 8.2 us against 14.3, 1024 x 8192 14.3 against
-// 26.6, 10240 x 8192 26.6 against 28.7; with 16 rows of one matrix the engine is
-// as fast, with more it is faster, so up to 8 rows come here.
+// warps (eight or four) share the contraction and add up in shared memory, so every
+// SM streams (24 warps, 16-byte loads, the next step's in flight under this one's
+// products). Device time by events (about 4 us of it the events'), one row, 8-bit
+// weights: 2560 x 2048 8.2 us against 14.3, 1024 x 8192 14.3 against 26.6, 10240 x
+// 8192 26.6 against 28.7; with 16 rows of one matrix the engine is as fast, with more
+// it is faster, so up to 8 rows come here. Back to back (launches overlapping) those
+// three take 3.8, 5.9 and 21.3 us (4 TB/s: a launch's start and end cost 4 us of it).
+// Deeper rings of asynchronous copies in shared memory measured the same for one row
+// and worse for eight (29 us against 22: the activations are read again per CTA).
 //
 // The multiplications are warp-level MMAs (m16n8, 16 features x 8 rows), which
 // cost next to nothing beside the weight stream; on plain FMAs eight rows would
@@ -28,8 +31,7 @@ namespace lmoe {
 namespace {
 
 constexpr int kFewFeats = 16;
-constexpr int kFewThreads = 256;
-constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewSmWarps = 24;  // resident per SM: 80 registers a thread
 static_assert(kFewRows <= 8, "one MMA's columns hold all rows");
 
 struct FewParams {
@@ -80,8 +82,9 @@ __device__ __forceinline__ int few_scan(int v, int* wsum) {
 // the last group as {n_groups, first, rows} for slot = P.slots; no rows if there
 // is none. Counts as in the engine: negative ones are 0, rows past n_rows do not
 // exist.
+template <int kWarps>
 __device__ __forceinline__ int3 find_group(const FewParams& P, int slot, int* wsum, int* found) {
-    constexpr int kPer = kMaxE / kFewThreads;
+    constexpr int kPer = kMaxE / (32 * kWarps);
     if (threadIdx.x < 3) found[threadIdx.x] = 0;
     int c[kPer], rows = 0;
 #pragma unroll
@@ -110,7 +113,7 @@ __device__ __forceinline__ int3 find_group(const FewParams& P, int slot, int* ws
         }
         at += c[i];
     }
-    if (slot == P.slots && threadIdx.x == kFewThreads - 1) {
+    if (slot == P.slots && threadIdx.x == 32 * kWarps - 1) {
         const int total = min(end, P.n_rows);
         found[0] = P.n_groups;
         found[1] = total;
@@ -127,52 +130,53 @@ struct Step {
     float s0, s1;
 };
 
-template <bool kF8>
-__global__ void __launch_bounds__(kFewThreads, 3) k_few(const FewParams P) {
+template <bool kF8, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const FewParams P) {
     constexpr int kStep = kF8 ? 128 : 64;  // contraction elements per step
-    __shared__ float red[kFewWarps][kFewFeats][9];
-    __shared__ int wsum[kFewWarps], found[3];
+    __shared__ float red[kWarps][kFewFeats][9];
+    __shared__ int wsum[kWarps], found[3];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int3 grp = make_int3(0, 0, P.n_rows);
-    if (P.counts) grp = find_group(P, blockIdx.y, wsum, found);
+    dependent_wait_and_release();
+    if (P.counts) grp = find_group<kWarps>(P, blockIdx.y, wsum, found);
     if (grp.z <= 0) return;
     const int f0 = blockIdx.x * kFewFeats;
     const long long row_bytes = (long long)P.cdim * (kF8 ? 1 : 2);
     const bool real = grp.x < P.n_groups;  // else zeros
     const int steps = real ? (P.cdim + kStep - 1) / kStep : 0;
     const int e = real ? grp.x : 0;
-    // the lane's two weight rows (the last one again past the end: its results are not stored)
-    const uint8_t* w0 = P.w + ((long long)e * P.feat + min(f0 + g, P.feat - 1)) * row_bytes + t * 16;
-    const uint8_t* w1 = P.w + ((long long)e * P.feat + min(f0 + g + 8, P.feat - 1)) * row_bytes + t * 16;
+    // the lane's two weight rows, w8 bytes apart (past the end the first one again: its results are not stored)
+    const uint8_t* w0 = P.w + ((long long)e * P.feat + f0 + g) * row_bytes + t * 16;
+    const long long w8 = f0 + 8 < P.feat ? 8 * row_bytes : 0;
     const float* ws = kF8 ? P.w_scale + ((long long)e * ((P.feat + 127) / 128) + f0 / 128) * steps : nullptr;
 
     const bool has = g < grp.z;  // the lane's activation row
     const uint8_t* xr = P.x + (long long)(grp.y + (has ? g : 0)) * P.ldx + t * 16;
     const int c = 2 * t;       // the lane's output rows: columns 2 t and 2 t + 1 of the MMA
     const float* xs = kF8 ? P.x_scale + (long long)(grp.y + min(c, grp.z - 1)) * steps : nullptr;
-    const float* xs1 = kF8 ? P.x_scale + (long long)(grp.y + min(c + 1, grp.z - 1)) * steps : nullptr;
+    const int xs1 = c + 1 < grp.z ? steps : 0;
     auto load = [&](int s, Step& v) {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         const long long at = (long long)s * 128;
         const bool in0 = s < steps && at + t * 16 < row_bytes, in1 = s < steps && at + 64 + t * 16 < row_bytes;
         v.a[0] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at)) : zero;
-        v.a[1] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w1 + at)) : zero;
+        v.a[1] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8)) : zero;
         v.a[2] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + 64)) : zero;
-        v.a[3] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w1 + at + 64)) : zero;
+        v.a[3] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8 + 64)) : zero;
         v.b[0] = in0 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at)) : zero;
         v.b[1] = in1 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at + 64)) : zero;
         if (kF8 && s < steps) {
             const float sw = __ldg(ws + s);
             v.s0 = __ldg(xs + s) * sw;
-            v.s1 = __ldg(xs1 + s) * sw;
+            v.s1 = __ldg(xs + xs1 + s) * sw;
         }
     };
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     Step v;
     load(warp, v);
-    for (int s = warp; s < steps; s += kFewWarps) {
+    for (int s = warp; s < steps; s += kWarps) {
         const Step q = v;
-        if (s + kFewWarps < steps) load(s + kFewWarps, v);
+        if (s + kWarps < steps) load(s + kWarps, v);
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         float(&o)[4] = kF8 ? d : acc;
         mma_16x8<kF8>(o, q.a[0].x, q.a[1].x, q.a[0].y, q.a[1].y, q.b[0].x, q.b[0].y);
@@ -191,12 +195,13 @@ __global__ void __launch_bounds__(kFewThreads, 3) k_few(const FewParams P) {
     red[warp][g + 8][2 * t] = acc[2];
     red[warp][g + 8][2 * t + 1] = acc[3];
     __syncthreads();
+    static_assert(32 * kWarps >= kFewFeats * 8, "a thread per output");
     if (threadIdx.x < kFewFeats * 8) {
         const int f = threadIdx.x % kFewFeats, r = threadIdx.x / kFewFeats;
         if (f0 + f < P.feat && r < grp.z) {
             float v = 0.f;
 #pragma unroll
-            for (int q = 0; q < kFewWarps; ++q) v += red[q][f][r];
+            for (int q = 0; q < kWarps; ++q) v += red[q][f][r];
             const long long o = (long long)(grp.y + r) * P.ldo + f0 + f;
             if (P.out_f32) static_cast<float*>(P.out)[o] = v;
             else static_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(v);
@@ -224,9 +229,15 @@ cudaError_t launch_few(bool f8, const void* w, const void* x, long long ldx_byte
     P.out_f32 = G.out_f32;
     P.zero_tail = G.zero_tail;
     const dim3 grid((G.feat + kFewFeats - 1) / kFewFeats, P.slots + (G.counts && G.zero_tail ? 1 : 0));
-    if (f8) k_few<true><<<grid, kFewThreads, 0, s>>>(P);
-    else k_few<false><<<grid, kFewThreads, 0, s>>>(P);
-    return cudaGetLastError();
+    // Four warps per CTA where that still fills the SMs (more than a wave of eight-warp CTAs): twice as many
+    // CTAs are resident, so the last wave wastes less (8 rows in 8 of 64 groups, 5120 x 2048, 8-bit 28.4 ->
+    // 22.5 us; 128 groups of 2560 x 2048 15.3 -> 13.8; 10240 x 8192 21.8 -> 21.3). Eight where the grid is
+    // small, so that a CTA's contraction is shared by more (1024 x 8192: 5.9 us against 8.7).
+    if ((long long)grid.x * grid.y > (long long)tc_num_sms() * (kFewSmWarps / 8))
+        return f8 ? launch_dependent(k_few<true, 4>, grid, 128, 0, 0, s, P)
+                  : launch_dependent(k_few<false, 4>, grid, 128, 0, 0, s, P);
+    return f8 ? launch_dependent(k_few<true, 8>, grid, 256, 0, 0, s, P)
+              : launch_dependent(k_few<false, 8>, grid, 256, 0, 0, s, P);
 }
 
 }  // namespace lmoe

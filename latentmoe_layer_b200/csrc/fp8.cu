@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const void* x, long long 
     const int row = blockIdx.x * 16 + (threadIdx.x >> 4), kb0 = blockIdx.y * kU;
     const int col0 = kb0 * 128 + sub * 8;
     const bool in_rows = row < rows;
+    dependent_wait_and_release();
     Eight<kF32> v[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(512) k_quantize_blocks(const void* x, long lon
     const int col = kb * 128 + (threadIdx.x & 15) * 8;
     Eight<kF32> v[4];
     uint32_t m = 0u;
+    dependent_wait_and_release();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int row = rb * 128 + u * 32 + (threadIdx.x >> 4);
@@ -157,10 +159,9 @@ cudaError_t launch_rows(const void* x, long long ldx, int rows, int cols, uint8_
     // as many blocks per half warp as a row fills, unless that leaves SMs without work
     // (64 rows of 8192: 6.1 us with four, 4.9 with one)
     if (kblocks >= 4 && (long long)gx * ((kblocks + 3) / 4) >= 2 * tc_num_sms())
-        k_quantize_rows<kF32, 4><<<dim3(gx, (kblocks + 3) / 4), 256, 0, s>>>(x, ldx, rows, cols, codes, scales);
-    else
-        k_quantize_rows<kF32, 1><<<dim3(gx, kblocks), 256, 0, s>>>(x, ldx, rows, cols, codes, scales);
-    return cudaGetLastError();
+        return launch_dependent(k_quantize_rows<kF32, 4>, dim3(gx, (kblocks + 3) / 4), 256, 0, 0, s, x, ldx, rows, cols,
+                                codes, scales);
+    return launch_dependent(k_quantize_rows<kF32, 1>, dim3(gx, kblocks), 256, 0, 0, s, x, ldx, rows, cols, codes, scales);
 }
 
 }  // namespace
@@ -172,12 +173,10 @@ cudaError_t launch_quantize_fp8(const void* x, bool f32, long long ldx, int n_ma
         // the matrices' rows follow each other with the same pitch
         return f32 ? launch_rows<true>(x, ldx, n_mat * rows, cols, codes, scales, s)
                    : launch_rows<false>(x, ldx, n_mat * rows, cols, codes, scales, s);
-    } else {
-        const dim3 grid(kblocks, (rows + 127) / 128, n_mat);
-        if (f32) k_quantize_blocks<true><<<grid, 512, 0, s>>>(x, ldx, rows, cols, codes, scales);
-        else k_quantize_blocks<false><<<grid, 512, 0, s>>>(x, ldx, rows, cols, codes, scales);
     }
-    return cudaGetLastError();
+    const dim3 grid(kblocks, (rows + 127) / 128, n_mat);
+    return f32 ? launch_dependent(k_quantize_blocks<true>, grid, 512, 0, 0, s, x, ldx, rows, cols, codes, scales)
+               : launch_dependent(k_quantize_blocks<false>, grid, 512, 0, 0, s, x, ldx, rows, cols, codes, scales);
 }
 
 }  // namespace lmoe

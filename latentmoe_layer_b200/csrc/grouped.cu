@@ -693,6 +693,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
         prefetch_tmap(&P.a_map);
         for (int i = 0; i < (kBMN ? 1 : 4); ++i) prefetch_tmap(&P.b_map[i]);
     }
+    dependent_wait_and_release();
     if (warp == 1) {
         tmem_alloc_pair(&S.tmem, 512);
         tmem_relinquish_pair();
@@ -1035,20 +1036,7 @@ cudaError_t launch_op(const GgParams& P, int clusters, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * P.splits * clusters);
-    cfg.blockDim = dim3(kGgThreads);
-    cfg.dynamicSmemBytes = kGgSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * P.splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_grouped<OP, kSplit>, P);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_dependent(k_grouped<OP, kSplit>, dim3(2 * P.splits * clusters), kGgThreads, kGgSmem, 2 * P.splits, s, P);
 }
 
 }  // namespace

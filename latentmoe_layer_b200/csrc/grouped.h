@@ -27,6 +27,28 @@ struct alignas(64) GgParams {
     unsigned spin;
 };
 
+// Launches a kernel as a dependent of the one before it in the stream: its launch and
+// set-up run under that kernel's end (dependent_wait_and_release in ptx.cuh). cluster 0: none.
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // GG_FWD (f8 = false) and GG_FP8 for up to kFewRows rows, where the kernel that splits a matrix over
 // all SMs is the faster one (few.cu has both sides' times); P's tensor maps are not used.
 constexpr int kFewRows = 8;

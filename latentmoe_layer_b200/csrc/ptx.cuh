@@ -118,6 +118,17 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel launched as a dependent may start while the kernel before it in the
+// stream still runs. It must not touch global memory that others write, nor
+// allocate TMEM (which that kernel's CTAs may still have to get), before this
+// wait, which returns once that kernel has completed and its writes are
+// visible. Called by every thread. Its own dependents are let in only after it,
+// so at most two kernels of a stream overlap.
+__device__ __forceinline__ void dependent_wait_and_release() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- clusters (2-SM pairs)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
