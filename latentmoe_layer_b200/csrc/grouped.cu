@@ -328,12 +328,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 // Zeros the rows from rem to the next multiple of 16 (the MMAs' depth; rows behind
 // that are not multiplied) of `subs` sub-tiles of 128-byte rows: 64 threads. Whole
 // rows, so the swizzle, which stays inside a row, does not matter.
@@ -354,15 +348,15 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// Waits for the loads so far; the registers pass through so that no use moves ahead of it.
-__device__ __forceinline__ void tmem_ld_wait32(uint32_t* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
+// Waits for the loads so far. The uses of their registers (below) are volatile too, which
+// keeps the compiler from moving them ahead of it.
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// acc += (lo, hi) and acc += (lo, hi) * s for registers that a load has written.
+__device__ __forceinline__ void add_loaded(uint64_t& acc, uint32_t lo, uint32_t hi) {
+    asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tadd.rn.f32x2 %0, %0, v;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi));
+}
+__device__ __forceinline__ void fma_loaded(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+    asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
 }
 // Four consecutive k-blocks' scales of one operand row, zero past its `left` last ones.
 __device__ __forceinline__ float4 load_scales(const float* p, int left, bool wide) {
@@ -470,7 +464,7 @@ __device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const fl
             tmem_ld_16x32(taddr + (uint32_t)(32 * g), r);
             tmem_ld_16x32(taddr + (uint32_t)(32 * g) + (16u << 16), r + 16);
         }
-        tmem_ld_wait32(r);
+        tmem_ld_wait();
         if (g + 1 < NG) {
             if (kAhead) {
                 uint32_t* n = raw[kAhead ? (g + 1) & 1 : 0];
@@ -489,7 +483,8 @@ __device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const fl
             for (int i = 0; i < 4; ++i) {
                 uint64_t& a = acc[i >> 1][4 * g + b][i & 1];
                 const uint32_t* v = r + 16 * (i >> 1) + 4 * b + 2 * (i & 1);
-                a = kF8 ? fma2(pack2(v[0], v[1]), s2, a) : add2(a, pack2(v[0], v[1]));
+                if (kF8) fma_loaded(a, v[0], v[1], s2);
+                else add_loaded(a, v[0], v[1]);
             }
         }
     }
@@ -516,7 +511,7 @@ __device__ __forceinline__ void drain_rows(uint64_t (&acc)[64], uint32_t taddr, 
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         uint32_t* r = raw[g & 1];
-        tmem_ld_wait32(r);
+        tmem_ld_wait();
         if (g + 1 < NG) {
             tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
             tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1) + 16), &raw[(g + 1) & 1][16]);
@@ -526,13 +521,15 @@ __device__ __forceinline__ void drain_rows(uint64_t (&acc)[64], uint32_t taddr, 
             mbar_arrive_bare(release, lane == 0);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[16 * g + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), s2, acc[16 * g + i]);
+        for (int i = 0; i < 16; ++i) fma_loaded(acc[16 * g + i], r[2 * i], r[2 * i + 1], s2);
     }
 }
 
 // GG_FP8_ROWS: a warp holds 32 rows (a lane each) x 128 features of one weight
 // block, so a 128-deep block's factor sx * sw is one register per thread and the
-// drain touches no shared memory, whose bandwidth the MMA's operands use up.
+// drain touches no shared memory, whose bandwidth the MMA's operands use up. It reads
+// all 128 columns even of a narrower tile: one straight path instead of a choice by
+// width took the dense prompt (16384 x 10240 x 8192) from 1504 to 1425 us.
 __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, int pair, int npairs, int ntiles,
                                               uint32_t crank, int q, int h, int lane, uint32_t tmem_base, uint32_t cempty0) {
     const uint32_t rank = crank & 1u;
@@ -546,7 +543,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
     };
     for (int t = pair; t < ntiles; t += npairs) {
         const GgTile ti = decode<GG_FP8_ROWS>(P, S, t, e, 0, 1);
-        const int c0 = h * 128, hc = min(128, max(0, ti.neff - c0));  // the warp's columns
+        const int c0 = h * 128;  // the warp's first column
         uint64_t acc[64];  // columns 2 i and 2 i + 1
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0ull;
@@ -569,13 +566,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
             free_stage();
             tc_fence_after();
             const uint32_t release = cempty0 + 8u * (uint32_t)buf, at = taddr + (uint32_t)(buf * kGgBN);
-            switch (hc) {
-                case 128: drain_rows<4>(acc, at, s, release, lane); break;
-                case 96: drain_rows<3>(acc, at, s, release, lane); break;
-                case 64: drain_rows<2>(acc, at, s, release, lane); break;
-                case 32: drain_rows<1>(acc, at, s, release, lane); break;
-                default: mbar_arrive_bare(release, lane == 0);
-            }
+            drain_rows<4>(acc, at, s, release, lane);  // columns past the matrix come from earlier blocks and are not stored
             if (++buf == 2) {
                 buf = 0;
                 bphase ^= 1u;
