@@ -7,14 +7,14 @@
 // 256-feature tile to a pair of SMs and keeps the tile's whole contraction there:
 // a 1024 x 8192 matrix is 4 tiles, for 74 pairs. Here a CTA takes 16 features, its
 // warps (eight or four) share the contraction and add up in shared memory, so every
-// SM streams (24 warps, 16-byte loads, the next step's in flight under this one's
+// SM streams (24 warps, 16-byte loads, the next steps' in flight under this one's
 // products). Device time by events (about 4 us of it the events'), one row, 8-bit
 // weights: 2560 x 2048 8.2 us against 14.3, 1024 x 8192 14.3 against 26.6, 10240 x
 // 8192 26.6 against 28.7; with 16 rows of one matrix the engine is as fast, with more
 // it is faster, so up to 8 rows come here. Back to back (launches overlapping) those
-// three take 3.8, 5.9 and 21.3 us (4 TB/s: a launch's start and end cost 4 us of it).
-// Deeper rings of asynchronous copies in shared memory measured the same for one row
-// and worse for eight (29 us against 22: the activations are read again per CTA).
+// three take 3.8, 5.8 and 18.3 us (4.6 TB/s; a launch's start and end are 4 us of it).
+// Measured no better: three to five steps ahead, the activations through the ring too (eight
+// rows 29 us against 21), and CTAs that start at different places of the contraction.
 //
 // The multiplications are warp-level MMAs (m16n8, 16 features x 8 rows), which
 // cost next to nothing beside the weight stream; on plain FMAs eight rows would
@@ -23,6 +23,8 @@
 // weight row are the A fragments of two MMAs as they come, and the same 16 bytes
 // of an activation row are their B fragments.
 #include <cuda_bf16.h>
+
+#include <atomic>
 
 #include "grouped.h"
 #include "ptx.cuh"
@@ -123,14 +125,17 @@ __device__ __forceinline__ int3 find_group(const FewParams& P, int slot, int* ws
     return make_int3(found[0], found[1], found[2]);
 }
 
-// One warp step's operands: 128 bytes of 16 weight rows and of 8 activation rows,
-// and the 8-bit scales of the lane's two output rows.
-struct Step {
-    uint4 a[4], b[2];
-    float s0, s1;
-};
+// 16 bytes to shared memory, asynchronously; zeros where there is nothing to read.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool in) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 
-template <bool kF8, int kWarps>
+// The weights of a warp step (128 bytes of 16 rows) are four 16-byte pieces per thread. They
+// come straight into registers, one step ahead, or (kRing) through shared memory, two
+// steps ahead: [stage][piece][thread], each copied and read by its thread alone.
+constexpr int kFewPieces = 4;
+
+template <bool kF8, int kWarps, bool kRing>
 __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const FewParams P) {
     constexpr int kStep = kF8 ? 128 : 64;  // contraction elements per step
     __shared__ float red[kWarps][kFewFeats][9];
@@ -155,41 +160,82 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
     const int c = 2 * t;       // the lane's output rows: columns 2 t and 2 t + 1 of the MMA
     const float* xs = kF8 ? P.x_scale + (long long)(grp.y + min(c, grp.z - 1)) * steps : nullptr;
     const int xs1 = c + 1 < grp.z ? steps : 0;
-    auto load = [&](int s, Step& v) {
+    extern __shared__ uint4 ring[];
+    constexpr int kThreads = 32 * kWarps;
+    const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+    uint4 na[kFewPieces], nb[2];
+    auto fetch = [&](int s, int stage) {  // step s's weights
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         const long long at = (long long)s * 128;
         const bool in0 = s < steps && at + t * 16 < row_bytes, in1 = s < steps && at + 64 + t * 16 < row_bytes;
-        v.a[0] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at)) : zero;
-        v.a[1] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8)) : zero;
-        v.a[2] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + 64)) : zero;
-        v.a[3] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8 + 64)) : zero;
-        v.b[0] = in0 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at)) : zero;
-        v.b[1] = in1 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at + 64)) : zero;
+        if (kRing) {
+            const uint8_t* p0 = w0 + (in0 ? at : 0);
+            const uint8_t* p1 = w0 + (in1 ? at + 64 : 0);
+            const uint32_t to = mine + (uint32_t)(stage * kFewPieces * kThreads * 16);
+            copy16(to, p0, in0);
+            copy16(to + kThreads * 16, p0 + w8, in0);
+            copy16(to + 2 * kThreads * 16, p1, in1);
+            copy16(to + 3 * kThreads * 16, p1 + w8, in1);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+            na[0] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at)) : zero;
+            na[1] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8)) : zero;
+            na[2] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + 64)) : zero;
+            na[3] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8 + 64)) : zero;
+        }
+    };
+    float n0 = 0.f, n1 = 0.f;
+    auto load = [&](int s) {  // and its activations and scales
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        const long long at = (long long)s * 128;
+        const bool in0 = s < steps && at + t * 16 < row_bytes, in1 = s < steps && at + 64 + t * 16 < row_bytes;
+        nb[0] = in0 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at)) : zero;
+        nb[1] = in1 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at + 64)) : zero;
         if (kF8 && s < steps) {
             const float sw = __ldg(ws + s);
-            v.s0 = __ldg(xs + s) * sw;
-            v.s1 = __ldg(xs + xs1 + s) * sw;
+            n0 = __ldg(xs + s) * sw;
+            n1 = __ldg(xs + xs1 + s) * sw;
         }
     };
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    Step v;
-    load(warp, v);
+    fetch(warp, 0);
+    if (kRing) fetch(warp + kWarps, 1);
+    load(warp);
+    int stage = 0;
     for (int s = warp; s < steps; s += kWarps) {
-        const Step q = v;
-        if (s + kWarps < steps) load(s + kWarps, v);
+        uint4 a[kFewPieces];
+        const uint4 b[2] = {nb[0], nb[1]};
+        const float s0 = n0, s1 = n1;
+#pragma unroll
+        for (int i = 0; i < kFewPieces; ++i) a[i] = na[i];
+        if (s + kWarps < steps) {
+            if (!kRing) fetch(s + kWarps, 0);
+            load(s + kWarps);
+        }
+        if (kRing) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < kFewPieces; ++i) a[i] = ring[(stage * kFewPieces + i) * kThreads + threadIdx.x];
+        }
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         float(&o)[4] = kF8 ? d : acc;
-        mma_16x8<kF8>(o, q.a[0].x, q.a[1].x, q.a[0].y, q.a[1].y, q.b[0].x, q.b[0].y);
-        mma_16x8<kF8>(o, q.a[0].z, q.a[1].z, q.a[0].w, q.a[1].w, q.b[0].z, q.b[0].w);
-        mma_16x8<kF8>(o, q.a[2].x, q.a[3].x, q.a[2].y, q.a[3].y, q.b[1].x, q.b[1].y);
-        mma_16x8<kF8>(o, q.a[2].z, q.a[3].z, q.a[2].w, q.a[3].w, q.b[1].z, q.b[1].w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mma_16x8<kF8>(o, a[2 * h].x, a[2 * h + 1].x, a[2 * h].y, a[2 * h + 1].y, b[h].x, b[h].y);
+            mma_16x8<kF8>(o, a[2 * h].z, a[2 * h + 1].z, a[2 * h].w, a[2 * h + 1].w, b[h].z, b[h].w);
+        }
         if (kF8) {
-            acc[0] = fmaf(d[0], q.s0, acc[0]);
-            acc[1] = fmaf(d[1], q.s1, acc[1]);
-            acc[2] = fmaf(d[2], q.s0, acc[2]);
-            acc[3] = fmaf(d[3], q.s1, acc[3]);
+            acc[0] = fmaf(d[0], s0, acc[0]);
+            acc[1] = fmaf(d[1], s1, acc[1]);
+            acc[2] = fmaf(d[2], s0, acc[2]);
+            acc[3] = fmaf(d[3], s1, acc[3]);
+        }
+        if (kRing) {
+            fetch(s + 2 * kWarps, stage);
+            stage ^= 1;
         }
     }
+    if (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
     red[warp][g][2 * t] = acc[0];
     red[warp][g][2 * t + 1] = acc[1];
     red[warp][g + 8][2 * t] = acc[2];
@@ -207,6 +253,29 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
             else static_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(v);
         }
     }
+}
+
+// A grid of four-warp CTAs that fits at once. It is given as much shared memory per CTA as
+// leaves room for ceil(grid / SMs) of them: with more room the next launch's CTAs, which
+// may come in early, would settle unevenly in the gaps, and that launch then wait for the
+// fullest SM.
+template <bool kF8>
+cudaError_t launch_ring(const FewParams& P, dim3 grid, int per_sm, cudaStream_t s) {
+    constexpr int kSmShared = 228 * 1024, kMost = 227 * 1024, kWarps = 4;
+    constexpr int kFixed = (int)sizeof(float) * kWarps * kFewFeats * 9 + 64 + 1024;  // static, and the system's
+    static_assert(kSmShared / (kFewSmWarps / kWarps) - kFixed - 640 >= 2 * kFewPieces * 32 * kWarps * 16, "the ring's room");
+    static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(k_few<kF8, kWarps, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost - kFixed);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    const int room = (kSmShared / per_sm - kFixed - 512) & ~127;
+    return launch_dependent(k_few<kF8, kWarps, true>, grid, 32 * kWarps, room < kMost - kFixed ? room : kMost - kFixed, 0, s, P);
 }
 
 }  // namespace
@@ -229,15 +298,19 @@ cudaError_t launch_few(bool f8, const void* w, const void* x, long long ldx_byte
     P.out_f32 = G.out_f32;
     P.zero_tail = G.zero_tail;
     const dim3 grid((G.feat + kFewFeats - 1) / kFewFeats, P.slots + (G.counts && G.zero_tail ? 1 : 0));
-    // Four warps per CTA where that still fills the SMs (more than a wave of eight-warp CTAs): twice as many
-    // CTAs are resident, so the last wave wastes less (8 rows in 8 of 64 groups, 5120 x 2048, 8-bit 28.4 ->
-    // 22.5 us; 128 groups of 2560 x 2048 15.3 -> 13.8; 10240 x 8192 21.8 -> 21.3). Eight where the grid is
-    // small, so that a CTA's contraction is shared by more (1024 x 8192: 5.9 us against 8.7).
-    if ((long long)grid.x * grid.y > (long long)tc_num_sms() * (kFewSmWarps / 8))
-        return f8 ? launch_dependent(k_few<true, 4>, grid, 128, 0, 0, s, P)
-                  : launch_dependent(k_few<false, 4>, grid, 128, 0, 0, s, P);
-    return f8 ? launch_dependent(k_few<true, 8>, grid, 256, 0, 0, s, P)
-              : launch_dependent(k_few<false, 8>, grid, 256, 0, 0, s, P);
+    // Eight warps per CTA where all those CTAs fit at once: its contraction is shared by more (1024 x 8192, one
+    // row: 5.8 us; four warps 8.7, the ring 7.2). Beyond that four, as twice as many CTAs are resident: through
+    // the ring, two steps ahead, while they fit at once (10240 x 8192, 8-bit: 18.3 us, registers 20.8, eight
+    // warps 21.8; 8192 x 8192 bf16 25.3, 33.2, 32.6), else through registers (8 rows in 8 of 64 groups, 5120 x
+    // 2048, 8-bit: 22.0, ring 23.1, eight warps 28.4).
+    const long long ctas = (long long)grid.x * grid.y, per_sm = (ctas + tc_num_sms() - 1) / tc_num_sms();
+    if (per_sm <= kFewSmWarps / 8)
+        return f8 ? launch_dependent(k_few<true, 8, false>, grid, 256, 0, 0, s, P)
+                  : launch_dependent(k_few<false, 8, false>, grid, 256, 0, 0, s, P);
+    if (per_sm <= kFewSmWarps / 4)
+        return f8 ? launch_ring<true>(P, grid, (int)per_sm, s) : launch_ring<false>(P, grid, (int)per_sm, s);
+    return f8 ? launch_dependent(k_few<true, 4, false>, grid, 128, 0, 0, s, P)
+              : launch_dependent(k_few<false, 4, false>, grid, 128, 0, 0, s, P);
 }
 
 }  // namespace lmoe
