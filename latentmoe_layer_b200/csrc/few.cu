@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
 // fullest SM.
 template <bool kF8>
 cudaError_t launch_ring(const FewParams& P, dim3 grid, int per_sm, cudaStream_t s) {
-    constexpr int kSmShared = 228 * 1024, kMost = 227 * 1024, kWarps = 4;
+    constexpr int kSmShared = 228 * 1024, kWarps = 4;
     constexpr int kFixed = (int)sizeof(float) * kWarps * kFewFeats * 9 + 64 + 1024;  // static, and the system's
     static_assert(kSmShared / (kFewSmWarps / kWarps) - kFixed - 640 >= 2 * kFewPieces * 32 * kWarps * 16, "the ring's room");
     static std::atomic<unsigned long long> ready{0};  // devices whose limit is set
@@ -270,12 +270,13 @@ cudaError_t launch_ring(const FewParams& P, dim3 grid, int per_sm, cudaStream_t 
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(k_few<kF8, kWarps, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost - kFixed);
+        e = cudaFuncSetAttribute(k_few<kF8, kWarps, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmShared / (kFewSmWarps / 8 + 1));  // per_sm is above kFewSmWarps / 8
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
     const int room = (kSmShared / per_sm - kFixed - 512) & ~127;
-    return launch_dependent(k_few<kF8, kWarps, true>, grid, 32 * kWarps, room < kMost - kFixed ? room : kMost - kFixed, 0, s, P);
+    return launch_dependent(k_few<kF8, kWarps, true>, grid, 32 * kWarps, room, 0, s, P);
 }
 
 }  // namespace

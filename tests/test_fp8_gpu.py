@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import latentmoe_layer_b200 as lm
-from test_grouped_gpu import HALF_STEP, spread
+from test_grouped_gpu import HALF_STEP, LARGE_GRIDS, spread
 
 pytestmark = pytest.mark.gpu
 F8 = torch.float8_e4m3fn
@@ -181,6 +181,23 @@ def test_few_rows_and_a_tail(counts, rows):
         lm.gemm_fp8(xq, xs, wq, ws, counts=c, out=y, zero_tail=zero_tail)
         check_product(y, xq, xs, wq, ws, counts)
         assert (y[used:] == (0.0 if zero_tail else -7.0)).all()
+
+
+@pytest.mark.parametrize("counts,N,K", LARGE_GRIDS, ids=["%dx%d e%d r%d" % (n, k, len(c), sum(c)) for c, n, k in LARGE_GRIDS])
+def test_few_rows_on_large_grids(counts, N, K):
+    K += K % 16
+    used = sum(counts)
+    rows = min(8, used + 1)
+    xq, xs, wq, ws, c = operands(counts, N, K, rows=rows)
+    xq.view(torch.uint8)[used:] = 0x7F
+    xs[used:] = float("nan")
+    for zero_tail in (False, True):
+        y = torch.full((rows, N), -7.0, device="cuda")
+        lm.gemm_fp8(xq, xs, wq, ws, counts=c, out=y, zero_tail=zero_tail)
+        check_product(y, xq, xs, wq, ws, counts)
+        assert (y[used:] == (0.0 if zero_tail else -7.0)).all()
+    if len(counts) == 1:
+        check_product(lm.gemm_fp8(xq[:used], xs[:used], wq[0], ws[0]), xq[:used], xs[:used], wq[0], ws[0], counts)
 
 
 def test_bad_values_stay_in_their_rows():

@@ -194,6 +194,26 @@ def test_few_rows_and_a_tail(counts, rows):
         check_forward(lm.grouped_gemm(x3, w3, c3), x3, w3, [first, second, rows - first - second])
 
 
+# CTAs of 16 columns and a group with rows: 148 SMs hold 444 of eight warps and 888 of four
+LARGE_GRIDS = [([1], 8200, 24), ([8], 8200, 1032), ([5], 14216, 520), ([2, 0, 3, 1], 2408, 2056), ([0, 1, 7], 5000, 72),
+               ([1, 2, 1, 1, 1, 1], 2456, 136), ([0, 1, 1, 2, 1, 1, 2], 2568, 712), ([3], 7112, 64), ([3], 14200, 200)]
+
+
+@pytest.mark.parametrize("counts,N,K", LARGE_GRIDS, ids=["%dx%d e%d r%d" % (n, k, len(c), sum(c)) for c, n, k in LARGE_GRIDS])
+@pytest.mark.parametrize("tail", [0, 2])
+def test_few_rows_on_large_grids(counts, N, K, tail):
+    rows = min(8, sum(counts) + tail)
+    x, _, w, c = make(counts, N, K, rows=rows)
+    used = sum(counts)
+    x[used:] = float("nan")
+    for dtype in (torch.bfloat16, torch.float32):
+        for zero_tail in (False, True):
+            y = torch.full((rows, N), -7.0, dtype=dtype, device="cuda")
+            lm.grouped_gemm(x, w, c, out=y, zero_tail=zero_tail)
+            check_forward(y, x, w, counts)
+            assert (y[used:] == (0.0 if zero_tail else -7.0)).all()
+
+
 def test_counts_that_do_not_fit():
     """Negative counts are empty groups; rows past the batch do not exist."""
     N, K = 72, 136
