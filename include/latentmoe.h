@@ -264,6 +264,8 @@ lmoe_status latentmoe_update_bias(lmoe_handle* h, const int32_t* expert_counts, 
  *  - Outputs are bf16 (one rounding from fp32, nearest-even) or fp32. NaN and
  *    infinities stay in the rows (for dw: in the group) that they belong to.
  *  - An output must not overlap an input.
+ *  - Stream order holds as for any kernel; a call's launch and set-up may run under
+ *    the end of the kernel before it, which it waits for before it touches memory.
  *  - A device wait that runs out of its bound is recorded process-wide and
  *    returned as LMOE_ERR_TIMEOUT by the next of these calls. */
 
