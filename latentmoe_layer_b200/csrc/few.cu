@@ -92,7 +92,7 @@ __device__ __forceinline__ int3 find_group(const FewParams& P, int slot, int* ws
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int g = (int)threadIdx.x * kPer + i;
-        c[i] = g < P.n_groups ? min(max(__ldg(P.counts + g), 0), P.n_rows) : 0;
+        c[i] = g < P.n_groups ? min(max(ld_global_s32(P.counts + g), 0), P.n_rows) : 0;
         rows += c[i];
     }
     const int end = few_scan(rows, wsum);  // at most 1024 x n_rows
@@ -178,10 +178,10 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
             copy16(to + 3 * kThreads * 16, p1 + w8, in1);
             asm volatile("cp.async.commit_group;" ::: "memory");
         } else {
-            na[0] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at)) : zero;
-            na[1] = in0 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8)) : zero;
-            na[2] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + 64)) : zero;
-            na[3] = in1 ? ld_global_nc_v4(reinterpret_cast<const uint4*>(w0 + at + w8 + 64)) : zero;
+            na[0] = in0 ? ld_global_v4(w0 + at) : zero;
+            na[1] = in0 ? ld_global_v4(w0 + at + w8) : zero;
+            na[2] = in1 ? ld_global_v4(w0 + at + 64) : zero;
+            na[3] = in1 ? ld_global_v4(w0 + at + w8 + 64) : zero;
         }
     };
     float n0 = 0.f, n1 = 0.f;
@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         const long long at = (long long)s * 128;
         const bool in0 = s < steps && at + t * 16 < row_bytes, in1 = s < steps && at + 64 + t * 16 < row_bytes;
-        nb[0] = in0 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at)) : zero;
-        nb[1] = in1 && has ? ld_global_nc_v4(reinterpret_cast<const uint4*>(xr + at + 64)) : zero;
+        nb[0] = in0 && has ? ld_global_v4(xr + at) : zero;
+        nb[1] = in1 && has ? ld_global_v4(xr + at + 64) : zero;
         if (kF8 && s < steps) {
-            const float sw = __ldg(ws + s);
-            n0 = __ldg(xs + s) * sw;
-            n1 = __ldg(xs + xs1 + s) * sw;
+            const float sw = ld_global_f32(ws + s);
+            n0 = ld_global_f32(xs + s) * sw;
+            n1 = ld_global_f32(xs + xs1 + s) * sw;
         }
     };
     float acc[4] = {0.f, 0.f, 0.f, 0.f};

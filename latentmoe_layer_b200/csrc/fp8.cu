@@ -29,8 +29,8 @@ struct Eight {
         if (kF32) w[kF32 ? 1 : 0] = make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ void load(const void* p) {  // 16-byte aligned
-        w[0] = ld_global_nc_v4(static_cast<const uint4*>(p));
-        if (kF32) w[kF32 ? 1 : 0] = ld_global_nc_v4(static_cast<const uint4*>(p) + 1);
+        w[0] = ld_global_v4(static_cast<const uint4*>(p));
+        if (kF32) w[kF32 ? 1 : 0] = ld_global_v4(static_cast<const uint4*>(p) + 1);
     }
     __device__ __forceinline__ uint32_t amax() const {
         if (kF32) {

@@ -118,12 +118,12 @@ __device__ __forceinline__ int build_groups(const GgParams& P, GgShared& S) {
     const int g0 = min(P.n_groups, (int)threadIdx.x * per), g1 = min(P.n_groups, g0 + per);
     long long mine = 0;
     for (int g = g0; g < g1; ++g)
-        mine += P.counts ? min(max(__ldg(P.counts + g), 0), P.n_rows) : P.n_rows;
+        mine += P.counts ? min(max(ld_global_s32(P.counts + g), 0), P.n_rows) : P.n_rows;
     long long end = block_scan(mine, S.wsum);
     long long at = end - mine;
     long long mt = 0;
     for (int g = g0; g < g1; ++g) {
-        const int c = P.counts ? min(max(__ldg(P.counts + g), 0), P.n_rows) : P.n_rows;
+        const int c = P.counts ? min(max(ld_global_s32(P.counts + g), 0), P.n_rows) : P.n_rows;
         const int lo = (int)min(at, (long long)P.n_rows), hi = (int)min(at + c, (long long)P.n_rows);
         S.off[g] = lo;
         mt += OP == GG_DW ? ceil_div(P.cols, kGgBN) : ceil_div(hi - lo, kGgBN);
@@ -135,7 +135,7 @@ __device__ __forceinline__ int build_groups(const GgParams& P, GgShared& S) {
     long long tat = tend - mt;
     at = end - mine;
     for (int g = g0; g < g1; ++g) {
-        const int c = P.counts ? min(max(__ldg(P.counts + g), 0), P.n_rows) : P.n_rows;
+        const int c = P.counts ? min(max(ld_global_s32(P.counts + g), 0), P.n_rows) : P.n_rows;
         const int lo = (int)min(at, (long long)P.n_rows), hi = (int)min(at + c, (long long)P.n_rows);
         S.tiles[g] = (int)tat;
         tat += (long long)ft * (OP == GG_DW ? ceil_div(P.cols, kGgBN) : ceil_div(hi - lo, kGgBN));
@@ -360,11 +360,14 @@ __device__ __forceinline__ void fma_loaded(uint64_t& acc, uint32_t lo, uint32_t 
 }
 // Four consecutive k-blocks' scales of one operand row, zero past its `left` last ones.
 __device__ __forceinline__ float4 load_scales(const float* p, int left, bool wide) {
-    if (wide) return __ldg(reinterpret_cast<const float4*>(p));
-    float4 s = make_float4(__ldg(p), 0.f, 0.f, 0.f);
-    if (left > 1) s.y = __ldg(p + 1);
-    if (left > 2) s.z = __ldg(p + 2);
-    if (left > 3) s.w = __ldg(p + 3);
+    if (wide) {
+        const uint4 v = ld_global_v4(p);
+        return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    float4 s = make_float4(ld_global_f32(p), 0.f, 0.f, 0.f);
+    if (left > 1) s.y = ld_global_f32(p + 1);
+    if (left > 2) s.z = ld_global_f32(p + 2);
+    if (left > 3) s.w = ld_global_f32(p + 3);
     return s;
 }
 

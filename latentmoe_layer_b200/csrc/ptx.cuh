@@ -78,6 +78,24 @@ __device__ __forceinline__ uint4 ld_global_nc_v4(const uint4* p) {
                  : "l"(p));
     return v;
 }
+// The same from global memory that another kernel may have written after this one was
+// launched (dependent launches, below): plain loads, as volatile asm, which stays behind
+// the wait for that kernel.
+__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int ld_global_s32(const int* p) {
+    int v;
+    asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float ld_global_f32(const float* p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
 // Streaming (evict-first) store: for data far larger than L2 that is written
 // once and read back later by another kernel.
 __device__ __forceinline__ void st_global_cs_v4(uint4* p, uint4 v) {
@@ -124,7 +142,9 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
 // allocate TMEM (which that kernel's CTAs may still have to get), before this
 // wait, which returns once that kernel has completed and its writes are
 // visible. Called by every thread. Its own dependents are let in only after it,
-// so at most two kernels of a stream overlap.
+// so at most two kernels of a stream overlap. What that kernel may have written
+// is not read-only for this one's life: read it with ld_global_* (or TMA, or
+// cp.async), not through the non-coherent path.
 __device__ __forceinline__ void dependent_wait_and_release() {
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }

@@ -1,0 +1,25 @@
+"""Memory-ordering rules that the products' kernels have to keep, checked in their sources. A break of one of
+them is not seen in results on every run, so it is looked for where it is written."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "latentmoe_layer_b200", "csrc")
+
+
+def code(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = f.read()
+    return re.sub(r"/\*.*?\*/", "", re.sub(r"//[^\n]*", "", text), flags=re.S)
+
+
+@pytest.mark.parametrize("name", ["grouped.cu", "few.cu", "fp8.cu"])
+def test_dependent_kernels_do_not_use_the_read_only_path(name):
+    """A kernel launched as a dependent is resident while the kernel before it still writes. Non-coherent
+    loads are for data that is read-only as long as the kernel lives, and a compiler may move them ahead of
+    the wait; operands, counts and scales are none of that."""
+    text = code(name)
+    assert "dependent_wait_and_release()" in text
+    assert not re.search(r"__ldg\b|ld_global_nc|ld\.global\.nc|__restrict__", text)
