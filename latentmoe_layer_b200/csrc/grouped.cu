@@ -272,16 +272,27 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
     return d;
 }
 
-// Arrive (where `on`) on a barrier of either CTA of the pair without a release: that
-// would first wait for the thread's own stores to global memory (1.3K to 3.7K cycles per
-// hand-over of a TMEM buffer). Nothing this thread wrote is handed over here: its
-// TMEM or shared-memory reads have completed. Predicated, so that the warp does
-// not branch.
-__device__ __forceinline__ void mbar_arrive_bare(uint32_t cluster_addr, bool on) {
+// Gives a buffer of TMEM back (the barrier may be the other CTA's) once the warp's loads
+// from it have completed (wait::ld). The fence orders them, so the arrival needs no
+// release, which would first wait for the thread's own stores to global memory (1.3K to
+// 3.7K cycles per hand-over at cluster scope). Predicated, so that the warp does not branch.
+__device__ __forceinline__ void release_tmem(uint32_t cluster_addr, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.u32 p, %1, 0;\n\t"
+        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+        "r"(lane)
+        : "memory");
+}
+// Arrive (where `on`) on this CTA's barrier, with a release: what the warp read from shared
+// memory before may be overwritten after it. Predicated too.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool on) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr),
+        "@p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
         "r"((uint32_t)on)
         : "memory");
 }
@@ -475,9 +486,7 @@ __device__ __forceinline__ void drain_columns(Acc& acc, uint32_t taddr, const fl
                 tmem_ld_16x32(taddr + (uint32_t)(32 * (g + 1)) + (16u << 16), n + 16);
             }
         } else if (last) {
-            tc_fence_before();
-            __syncwarp();
-            mbar_arrive_bare(release, lane == 0);
+            release_tmem(release, lane);
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -519,9 +528,7 @@ __device__ __forceinline__ void drain_rows(uint64_t (&acc)[64], uint32_t taddr, 
             tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1)), &raw[(g + 1) & 1][0]);
             tmem_ld_32x16(taddr + (uint32_t)(32 * (g + 1) + 16), &raw[(g + 1) & 1][16]);
         } else {
-            tc_fence_before();
-            __syncwarp();
-            mbar_arrive_bare(release, lane == 0);
+            release_tmem(release, lane);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) fma_loaded(acc[16 * g + i], r[2 * i], r[2 * i + 1], s2);
@@ -534,14 +541,12 @@ __device__ __forceinline__ void drain_rows(uint64_t (&acc)[64], uint32_t taddr, 
 // all 128 columns even of a narrower tile: one straight path instead of a choice by
 // width took the dense prompt (16384 x 10240 x 8192) from 1504 to 1425 us.
 __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, int pair, int npairs, int ntiles,
-                                              uint32_t crank, int q, int h, int lane, uint32_t tmem_base, uint32_t cempty0) {
-    const uint32_t rank = crank & 1u;
+                                              uint32_t rank, int q, int h, int lane, uint32_t tmem_base, uint32_t cempty0) {
     int buf = 0, sbuf = 0, e = 0, stage = 0;
     uint32_t bphase = 0, sphase = 0;
     const bool frees = q == 0 && h == 0 && lane == 0;
-    const uint32_t empty0 = mapa_shared(&S.empty[0], crank), sempty0 = mapa_shared(&S.sempty[0], crank);
     auto free_stage = [&] {  // the block's operands have been read
-        mbar_arrive_bare(empty0 + 8u * (uint32_t)stage, frees);
+        mbar_arrive_if(&S.empty[stage], frees);
         if (++stage == kGgStages) stage = 0;
     };
     for (int t = pair; t < ntiles; t += npairs) {
@@ -556,7 +561,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
                 if (!mbar_wait_bounded(&S.sfull[sbuf], sphase, P.spin, P.err)) return;
                 f = *reinterpret_cast<const float4*>(&S.scale[sbuf][0][0] + 4 * (h * 128 + q * 32 + lane));
                 __syncwarp();
-                mbar_arrive_bare(sempty0 + 8u * (uint32_t)sbuf, lane == 0);
+                mbar_arrive_if(&S.sempty[sbuf], lane == 0);
                 if (++sbuf == 2) {
                     sbuf = 0;
                     sphase ^= 1u;
@@ -935,7 +940,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
         const int q = warp & 3, h = (warp - 4) >> 2;
         const uint32_t cempty0 = mapa_shared(&S.cempty[0], lead);
         if (kRowsM) {
-            epilogue_rows(P, S, pair, npairs, ntiles, crank, q, h, lane, tmem_base, cempty0);
+            epilogue_rows(P, S, pair, npairs, ntiles, rank, q, h, lane, tmem_base, cempty0);
         } else {
         int buf = 0, sbuf = 0, e = 0;
         uint32_t bphase = 0, sphase = 0;

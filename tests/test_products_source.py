@@ -23,3 +23,14 @@ def test_dependent_kernels_do_not_use_the_read_only_path(name):
     text = code(name)
     assert "dependent_wait_and_release()" in text
     assert not re.search(r"__ldg\b|ld_global_nc|ld\.global\.nc|__restrict__", text)
+
+
+def test_relaxed_arrivals_hand_over_tmem_only():
+    """An arrival without a release orders no earlier read of shared memory. It is allowed where a buffer of
+    TMEM is given back: wait::ld has completed the reads, and the fence before the arrival orders them."""
+    text = code("grouped.cu")
+    arrivals = [m.start() for m in re.finditer(r"arrive\.relaxed", text)]
+    assert len(arrivals) == 1
+    before = text[:arrivals[0]]
+    body = before[before.rindex("__device__"):]
+    assert "tc_fence_before();" in body and "__syncwarp();" in body and body.index("tc_fence_before") < body.index("__syncwarp")
