@@ -920,11 +920,12 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                     zero_rows(S.b[stage], ti.neff > 128 ? 2 : 1, ti.rem, tid);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    // the fence above hands the zeros to the MMA; a cluster-scope release on top of it
-                    // costs 7% of a training batch's weight gradient
-                    if (lane == 0)
-                        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(&S.tail[stage], lead))
-                                     : "memory");
+                    // the leader's MMAs read the zeros of both CTAs: the other one's have to be
+                    // released at cluster scope, to the issuer's wait of the same scope
+                    if (lane == 0) {
+                        if (leader) mbar_arrive(&S.tail[stage]);
+                        else mbar_arrive_cluster(mapa_shared(&S.tail[stage], lead));
+                    }
                 }
                 if (++stage == kGgStages) stage = 0;
             }

@@ -34,3 +34,11 @@ def test_relaxed_arrivals_hand_over_tmem_only():
     before = text[:arrivals[0]]
     body = before[before.rindex("__device__"):]
     assert "tc_fence_before();" in body and "__syncwarp();" in body and body.index("tc_fence_before") < body.index("__syncwarp")
+
+
+@pytest.mark.parametrize("name", ["grouped.cu", "ptx.cuh"])
+def test_arrivals_on_another_cta_name_their_scope(name):
+    """Without a scope an arrival releases to its own CTA alone; on a shared::cluster address the waiting
+    thread may be in another one."""
+    for m in re.finditer(r'"[^"\n]*mbarrier\.arrive[^"\n]*shared::cluster[^"\n]*"', code(name)):
+        assert re.search(r"arrive(\.expect_tx)?\.(release|relaxed)\.cluster", m.group()) or "tcgen05.commit" in m.group(), m.group()
