@@ -326,6 +326,19 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_
     return false;
 }
 
+// Bounded wait of a whole warp: all lanes see the phase completed, or all give up. (Lanes that
+// decide alone could part at the limit, ahead of a __syncwarp or a TMEM load that needs them all.)
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned limit, int* err) {
+    if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) return true;
+    for (unsigned i = 0; i < limit; ++i) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 4095u) == 4095u && __any_sync(0xFFFFFFFFu, *(volatile int*)err != 0)) return false;
+    }
+    if ((threadIdx.x & 31) == 0) atomicCAS(err, 0, 5);
+    __syncwarp();
+    return false;
+}
+
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
@@ -558,7 +571,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
         float4 f;
         for (int kb = 0; kb < ti.nkb; ++kb) {
             if (kb % kScaleBatch == 0) {
-                if (!mbar_wait_bounded(&S.sfull[sbuf], sphase, P.spin, P.err)) return;
+                if (!mbar_wait_warp(&S.sfull[sbuf], sphase, P.spin, P.err)) return;
                 f = *reinterpret_cast<const float4*>(&S.scale[sbuf][0][0] + 4 * (h * 128 + q * 32 + lane));
                 __syncwarp();
                 mbar_arrive_if(&S.sempty[sbuf], lane == 0);
@@ -570,7 +583,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
             const float s = f.x;
             f = make_float4(f.y, f.z, f.w, 0.f);
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
-            if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, P.err)) return;
+            if (!mbar_wait_warp(&S.cfull[buf], bphase, P.spin, P.err)) return;
             free_stage();
             tc_fence_after();
             const uint32_t release = cempty0 + 8u * (uint32_t)buf, at = taddr + (uint32_t)(buf * kGgBN);
@@ -870,7 +883,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                             v[i] = load_scales(P.b_scale + (long long)(ti.row0 + row) * kblocks + ti.kb0 + kb0, kblocks - ti.kb0 - kb0,
                                                wide);
                     }
-                    if (!mbar_wait_bounded(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
+                    if (!mbar_wait_warp(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
                         ok = false;
                         break;
                     }
@@ -911,7 +924,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                 if (ti.nkb == 0) continue;
                 stage = (stage + ti.nkb - 1) % kGgStages;  // of the tile's last k-block
                 if (ti.rem) {
-                    if (!mbar_wait_bounded(&S.landed[stage], (lphase >> stage) & 1u, P.spin, err)) {
+                    if (!mbar_wait_warp(&S.landed[stage], (lphase >> stage) & 1u, P.spin, err)) {
                         ok = false;
                         break;
                     }
@@ -955,11 +968,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
             const int ck = kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
             const int ng = (hc + 31) >> 5;  // 32-column groups; an odd 16 reads 16 columns that are not stored
             for (int kb0 = 0; kb0 < ti.nkb; kb0 += ck) {
-                if (kF8 && kb0 % kScaleBatch == 0 && !mbar_wait_bounded(&S.sfull[sbuf], sphase, P.spin, err)) {
+                if (kF8 && kb0 % kScaleBatch == 0 && !mbar_wait_warp(&S.sfull[sbuf], sphase, P.spin, err)) {
                     ok = false;
                     break;
                 }
-                if (!mbar_wait_bounded(&S.cfull[buf], bphase, P.spin, err)) {
+                if (!mbar_wait_warp(&S.cfull[buf], bphase, P.spin, err)) {
                     ok = false;
                     break;
                 }

@@ -42,3 +42,22 @@ def test_arrivals_on_another_cta_name_their_scope(name):
     thread may be in another one."""
     for m in re.finditer(r'"[^"\n]*mbarrier\.arrive[^"\n]*shared::cluster[^"\n]*"', code(name)):
         assert re.search(r"arrive(\.expect_tx)?\.(release|relaxed)\.cluster", m.group()) or "tcgen05.commit" in m.group(), m.group()
+
+
+def test_a_warp_gives_up_a_wait_as_a_whole():
+    """A wait that runs out for some lanes of a warp and not for others would send them different ways before
+    an instruction that needs all of them. Waits of single elected threads may decide alone; the others vote."""
+    text = code("grouped.cu")
+    roles = ["elect_one()) {", "warp >= 2 &&", "setmaxnreg.inc", "void epilogue_rows"]
+    single = [m.start() for m in re.finditer(r"\bif \(!?(?:mbar_)?wait_\w+\(|\b(?:mbar_)?wait_\w+\(&", text)]
+    checked = 0
+    for at in single:
+        name = re.search(r"(\w*wait_\w+)\(", text[at:]).group(1)
+        place = max((text.rfind(r, 0, at), r) for r in roles)
+        if place[0] < 0:
+            continue  # inside the waits themselves
+        checked += 1
+        assert ("warp" in name) == (place[1] != "elect_one()) {"), (name, place[1], text[at:at + 80])
+    assert checked >= 12
+    body = text[text.index("wait_warp("):]
+    assert "__all_sync" in body[:body.index("\n}\n")]
