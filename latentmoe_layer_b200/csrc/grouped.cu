@@ -46,7 +46,7 @@
 // the tensor maps.
 //
 // Every mbarrier wait is bounded; on running out the kernel records
-// LMOE_ERR_TIMEOUT, drains its own MMAs, frees TMEM and returns.
+// LMOE_ERR_TIMEOUT, its cluster waits for its own loads and MMAs, frees TMEM and returns.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -70,7 +70,7 @@ constexpr int kScaleBatch = 4;        // k-blocks per batch of scale products
 constexpr int kLaunchRegs = 168;
 template <int OP>
 struct GgRegs {
-    static constexpr int kProd = OP == GG_FP8 ? 72 : 56, kEpi = OP == GG_FP8 ? 216 : 224;
+    static constexpr int kProd = OP >= GG_FP8 ? 72 : 56, kEpi = OP >= GG_FP8 ? 216 : 224;
     static_assert(128 * kProd + 256 * kEpi <= 384 * kLaunchRegs, "register split");
 };
 
@@ -86,6 +86,9 @@ struct alignas(1024) GgShared {
     uint64_t landed[kGgStages], tail[kGgStages];  // GG_DW: a partial k-block is in this CTA's stage; its end is zero
     uint64_t cfull[2], cempty[2], sfull[2], sempty[2], done;
     uint32_t tmem;
+    int gave_up;               // a wait of this cluster ran out
+    int issued;                // k-blocks this CTA's producer has loaded
+    uint32_t sent[kGgStages];  // bytes of a stage's last load that are counted at the leader (partial k-blocks: 0)
 };
 constexpr size_t kGgSmem = sizeof(GgShared) + 1024;
 static_assert(kGgSmem <= 232448, "shared memory");
@@ -308,35 +311,62 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// try_wait that acquires at cluster scope: the arrivals come from both CTAs.
-__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, unsigned limit, int* err) {
-    for (unsigned i = 0; i < limit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if ((i & 4095u) == 4095u && *(volatile int*)err != 0) return false;
+// ---- Bounded waits. One that runs out makes the whole cluster give up (every CTA has the word,
+// polled in its own shared memory) and is counted for the host. Other clusters, and other
+// launches, go on: the word that the host reads is never read here.
+__device__ __forceinline__ void give_up(GgShared& S, const GgParams& P) {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+#pragma unroll 1
+    for (uint32_t r = 0; r < n; ++r)
+        asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(mapa_shared(&S.gave_up, r)) : "memory");
+    atomicCAS(P.err, 0, 5);
+}
+__device__ __forceinline__ bool gave_up(const GgShared& S) {
+    int v;
+    asm volatile("ld.relaxed.cluster.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(&S.gave_up)) : "memory");
+    return v != 0;
+}
+// try_wait that acquires at cluster scope: for arrivals of generic accesses in the other CTA.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait of one elected thread.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, GgShared& S, const GgParams& P) {
+    if (!kCluster && mbar_test_wait(bar, parity)) return true;
+    for (unsigned i = 0; i < P.spin; ++i) {
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if ((i & 255u) == 255u && gave_up(S)) return false;
     }
-    atomicCAS(err, 0, 5);
+    give_up(S, P);
     return false;
 }
-
-// Bounded wait of a whole warp: all lanes see the phase completed, or all give up. (Lanes that
+// Wait of a whole warp: all lanes see the phase completed, or all give up. (Lanes that
 // decide alone could part at the limit, ahead of a __syncwarp or a TMEM load that needs them all.)
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, unsigned limit, int* err) {
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, GgShared& S, const GgParams& P) {
     if (__all_sync(0xFFFFFFFFu, mbar_test_wait(bar, parity))) return true;
-    for (unsigned i = 0; i < limit; ++i) {
+    for (unsigned i = 0; i < P.spin; ++i) {
         if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-        if ((i & 4095u) == 4095u && __any_sync(0xFFFFFFFFu, *(volatile int*)err != 0)) return false;
+        if ((i & 255u) == 255u && __any_sync(0xFFFFFFFFu, gave_up(S))) return false;
     }
-    if ((threadIdx.x & 31) == 0) atomicCAS(err, 0, 5);
+    if ((threadIdx.x & 31) == 0) give_up(S, P);
     __syncwarp();
     return false;
+}
+// Wait for operations already under way, which end by themselves: does not leave when the
+// cluster gives up, and is bounded all the same.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+    for (unsigned i = 0; i < (1u << 24); ++i)
+        if (mbar_try_wait(bar, parity)) return;
 }
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -571,7 +601,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
         float4 f;
         for (int kb = 0; kb < ti.nkb; ++kb) {
             if (kb % kScaleBatch == 0) {
-                if (!mbar_wait_warp(&S.sfull[sbuf], sphase, P.spin, P.err)) return;
+                if (!wait_warp(&S.sfull[sbuf], sphase, S, P)) return;
                 f = *reinterpret_cast<const float4*>(&S.scale[sbuf][0][0] + 4 * (h * 128 + q * 32 + lane));
                 __syncwarp();
                 mbar_arrive_if(&S.sempty[sbuf], lane == 0);
@@ -583,7 +613,7 @@ __device__ __forceinline__ void epilogue_rows(const GgParams& P, GgShared& S, in
             const float s = f.x;
             f = make_float4(f.y, f.z, f.w, 0.f);
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
-            if (!mbar_wait_warp(&S.cfull[buf], bphase, P.spin, P.err)) return;
+            if (!wait_warp(&S.cfull[buf], bphase, S, P)) return;
             free_stage();
             tc_fence_after();
             const uint32_t release = cempty0 + 8u * (uint32_t)buf, at = taddr + (uint32_t)(buf * kGgBN);
@@ -672,6 +702,33 @@ __device__ __forceinline__ void add_partials(Acc& acc, const uint8_t* stages, in
     }
 }
 
+// How often n k-blocks in turn have used stage s.
+__device__ __forceinline__ int uses(int n, int s) { return n > s ? (n - s + kGgStages - 1) / kGgStages : 0; }
+
+// After the cluster gave up: waits for the pair's loads in flight. They are counted on the leader's
+// full barriers, each phase of which waits for the bytes of both CTAs; where only one CTA's
+// producer got to load a k-block, the other's share is made up here. (A CTA can be at most one
+// use of a stage ahead: reusing it takes an MMA that read both CTAs' operands.)
+__device__ void drain_loads(GgShared& S, uint32_t other) {
+    int theirs;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(theirs) : "r"(mapa_shared(&S.issued, other)) : "memory");
+#pragma unroll 1
+    for (int s = 0; s < kGgStages; ++s) {
+        const int u0 = uses(S.issued, s), u1 = uses(theirs, s);
+        uint32_t b1;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(b1) : "r"(mapa_shared(&S.sent[s], other)) : "memory");
+        if (u0 > u1 && S.sent[s])
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&S.full[s])), "r"(S.sent[s])
+                         : "memory");
+        if (u1 > u0) {
+            if (b1 == 0) continue;  // a partial k-block: counted in that CTA
+            mbar_arrive_expect_tx(&S.full[s], b1);
+        }
+        const int u = max(u0, u1);
+        if (u > 0) drain_wait(&S.full[s], (uint32_t)(u - 1) & 1u);
+    }
+}
+
 // kSplit: a cluster holds P.splits pairs, which share each tile's contraction. (An
 // instantiation of its own: ranks known at compile time keep the others' registers
 // free of spills, which cost the 8-bit products 15%.)
@@ -701,6 +758,8 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
             mbar_init(&S.sempty[b], kGgEpiWarps);
         }
         mbar_init(&S.done, 1);
+        S.gave_up = 0;
+        S.issued = 0;
         fence_mbar_init();
         prefetch_tmap(&P.a_map);
         for (int i = 0; i < (kBMN ? 1 : 4); ++i) prefetch_tmap(&P.b_map[i]);
@@ -715,14 +774,14 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
     cluster_sync_all();  // barriers, TMEM and tables of both CTAs are ready
     tc_fence_after();
     const uint32_t tmem_base = S.tmem;
-    int* err = P.err;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(GgRegs<OP>::kProd));
         if (warp == 0 && elect_one()) {
             // -------------------------------------------- TMA producer (both CTAs)
             int stage = 0, e = 0;
-            uint32_t phase = 0, issued = 0, issued_par = 0, partial = 0, partial_n = 0;
+            int issued = 0;
+            uint32_t phase = 0, partial = 0, partial_n = 0;
             const uint32_t full0 = mapa_shared(&S.full[0], lead);
             bool ok = true;
             for (int t = pair; t < ntiles && ok; t += npairs) {
@@ -731,7 +790,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                 const int b0 = (kBMN ? ti.col0 : ti.row0) + (int)rank * half;
                 const uint32_t bytes_b = kRowsM ? (uint32_t)kGgBBytes : kBMN ? (uint32_t)((half + 63) / 64) * 8192u : (uint32_t)half * 128u;
                 for (int kb = 0; kb < ti.nkb; ++kb) {
-                    if (!mbar_wait_bounded(&S.empty[stage], phase ^ 1u, P.spin, err)) {
+                    if (!wait_one(&S.empty[stage], phase ^ 1u, S, P)) {
                         ok = false;
                         break;
                     }
@@ -744,7 +803,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                         tma_load_3d(S.b[stage], &P.b_map[0], &S.landed[stage], b0, r, 0);
                         if (half > 64) tma_load_3d(S.b[stage] + 8192, &P.b_map[0], &S.landed[stage], b0 + 64, r, 0);
                         if (leader) mbar_arrive(&S.full[stage]);
-                        issued &= ~(1u << stage);  // the stage's earlier load has been consumed
+                        S.sent[stage] = 0;
                         partial |= 1u << stage;
                         partial_n ^= 1u << stage;
                     } else {
@@ -776,22 +835,23 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                                     r += 128 >> i;
                                 }
                         }
-                        issued |= 1u << stage;
-                        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                        S.sent[stage] = kGgABytes + bytes_b;
                     }
+                    ++issued;
                     if (++stage == kGgStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            // the leader's full barriers count both CTAs' bytes: waiting on them drains every
-            // load of the pair before either CTA can pass the final cluster barrier
-            for (int s = 0; s < kGgStages; ++s)  // the stage's last partial block has parity (their number - 1) % 2
-                if ((partial >> s) & 1u) mbar_wait_bounded(&S.landed[s], (~partial_n >> s) & 1u, 1u << 26, err);
-            if (leader)
+            S.issued = issued;
+            // every stage given back: its loads have landed and been read, and no arrival at
+            // this CTA's barriers is under way when it leaves
+            for (int s = 0; s < kGgStages && ok; ++s)
+                if (issued > s) ok = wait_one(&S.empty[s], uses(issued, s) - 1 & 1, S, P);
+            if (!ok)  // drain_loads does the rest; the stage's last partial block has parity (their number - 1) % 2
                 for (int s = 0; s < kGgStages; ++s)
-                    if ((issued >> s) & 1u) mbar_wait_bounded(&S.full[s], (issued_par >> s) & 1u, 1u << 26, err);
+                    if ((partial >> s) & 1u) drain_wait(&S.landed[s], (~partial_n >> s) & 1u);
         } else if (warp == 1 && leader && elect_one()) {
             // -------------------------------------------- MMA issuer (leader only)
             constexpr uint32_t type = kF8 ? 0u : 1u;  // e4m3 : bf16
@@ -806,7 +866,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                 const uint32_t idesc = idesc0 | ((uint32_t)(ti.neff >> 3) << 17);
                 const int ck = kRowsM ? 1 : kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
                 for (int kb0 = 0; kb0 < ti.nkb && ok; kb0 += ck) {
-                    if (!mbar_wait_bounded(&S.cempty[buf], bphase ^ 1u, P.spin, err)) {
+                    if (!wait_one(&S.cempty[buf], bphase ^ 1u, S, P)) {
                         ok = false;
                         break;
                     }
@@ -814,14 +874,14 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                     uint32_t d = tmem_base + (uint32_t)(buf * kGgBN);
                     const int kb1 = min(ti.nkb, kb0 + ck);
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!mbar_wait_bounded(&S.full[stage], phase, P.spin, err)) {
+                        if (!wait_one(&S.full[stage], phase, S, P)) {
                             ok = false;
                             break;
                         }
                         int steps = 4;
                         if (OP == GG_DW && ti.rem && kb == ti.nkb - 1) {
                             steps = (ti.rem + 15) >> 4;
-                            if (!mbar_wait_bounded_cluster(&S.tail[stage], (tphase >> stage) & 1u, P.spin, err)) {
+                            if (!wait_one<true>(&S.tail[stage], (tphase >> stage) & 1u, S, P)) {
                                 ok = false;
                                 break;
                             }
@@ -853,7 +913,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                 }
             }
             umma_commit_pair_self(&S.done);
-            mbar_wait_bounded(&S.done, 0, 1u << 26, err);
+            drain_wait(&S.done, 0);
         } else if (warp >= 2 && kF8) {
             // -------------------------------------------- scale products
             const int tid = threadIdx.x - 64;
@@ -883,7 +943,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                             v[i] = load_scales(P.b_scale + (long long)(ti.row0 + row) * kblocks + ti.kb0 + kb0, kblocks - ti.kb0 - kb0,
                                                wide);
                     }
-                    if (!mbar_wait_warp(&S.sempty[buf], bphase ^ 1u, P.spin, err)) {
+                    if (!wait_warp(&S.sempty[buf], bphase ^ 1u, S, P)) {
                         ok = false;
                         break;
                     }
@@ -924,7 +984,7 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
                 if (ti.nkb == 0) continue;
                 stage = (stage + ti.nkb - 1) % kGgStages;  // of the tile's last k-block
                 if (ti.rem) {
-                    if (!mbar_wait_warp(&S.landed[stage], (lphase >> stage) & 1u, P.spin, err)) {
+                    if (!wait_warp(&S.landed[stage], (lphase >> stage) & 1u, S, P)) {
                         ok = false;
                         break;
                     }
@@ -968,11 +1028,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
             const int ck = kF8 ? blocks_per_drain(ti.neff) : P.chunk_kb;
             const int ng = (hc + 31) >> 5;  // 32-column groups; an odd 16 reads 16 columns that are not stored
             for (int kb0 = 0; kb0 < ti.nkb; kb0 += ck) {
-                if (kF8 && kb0 % kScaleBatch == 0 && !mbar_wait_warp(&S.sfull[sbuf], sphase, P.spin, err)) {
+                if (kF8 && kb0 % kScaleBatch == 0 && !wait_warp(&S.sfull[sbuf], sphase, S, P)) {
                     ok = false;
                     break;
                 }
-                if (!mbar_wait_warp(&S.cfull[buf], bphase, P.spin, err)) {
+                if (!wait_warp(&S.cfull[buf], bphase, S, P)) {
                     ok = false;
                     break;
                 }
@@ -1027,6 +1087,11 @@ __global__ void __launch_bounds__(kGgThreads, 1) k_grouped(const __grid_constant
     tc_fence_before();
     cluster_sync_all();  // both CTAs done with TMEM and shared memory; the leader's MMAs have completed
     tc_fence_after();
+    if (gave_up(S)) {  // the same in all CTAs of the cluster: nobody gives up after the barrier
+        if (leader && threadIdx.x == 0) drain_loads(S, crank ^ 1u);
+        __syncthreads();
+        cluster_sync_all();
+    }
     if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
 }
 

@@ -48,16 +48,30 @@ def test_a_warp_gives_up_a_wait_as_a_whole():
     """A wait that runs out for some lanes of a warp and not for others would send them different ways before
     an instruction that needs all of them. Waits of single elected threads may decide alone; the others vote."""
     text = code("grouped.cu")
-    roles = ["elect_one()) {", "warp >= 2 &&", "setmaxnreg.inc", "void epilogue_rows"]
-    single = [m.start() for m in re.finditer(r"\bif \(!?(?:mbar_)?wait_\w+\(|\b(?:mbar_)?wait_\w+\(&", text)]
-    checked = 0
-    for at in single:
-        name = re.search(r"(\w*wait_\w+)\(", text[at:]).group(1)
-        place = max((text.rfind(r, 0, at), r) for r in roles)
-        if place[0] < 0:
-            continue  # inside the waits themselves
-        checked += 1
-        assert ("warp" in name) == (place[1] != "elect_one()) {"), (name, place[1], text[at:at + 80])
-    assert checked >= 12
+    roles = ["elect_one()) {", "void drain_loads", "warp >= 2 &&", "setmaxnreg.inc", "void epilogue_rows"]
+    waits = [(m.start(), m.group(1)) for m in re.finditer(r"\b(\w*wait\w*)(?:<\w+>)?\(&S\.", text)]
+    assert len(waits) >= 10
+    for at, name in waits:
+        role = max((text.rfind(r, 0, at), r) for r in roles)[1]
+        assert ("warp" in name) == (role not in roles[:2]), (name, role, text[at:at + 80])
     body = text[text.index("wait_warp("):]
     assert "__all_sync" in body[:body.index("\n}\n")]
+
+
+def test_waits_leave_on_a_word_of_their_own_launch():
+    """A kernel that gave up its waits because of a word shared by the process would be cut short by another
+    stream's failure, and once more at every replay of a graph. The word that reports to the host is written
+    by kernels and read by the host only."""
+    text = code("grouped.cu")
+    assert "*(volatile int*)err" not in text and "mbar_wait_bounded" not in text
+    assert "gave_up" in text[text.index("struct alignas(1024) GgShared"):text.index("constexpr size_t kGgSmem")]
+
+
+def test_final_drains_do_not_leave_early():
+    """The waits for MMAs and copies in flight, ahead of freeing TMEM and leaving, go on after a timeout."""
+    text = code("grouped.cu")
+    body = text[text.index("drain_wait("):]
+    body = body[:body.index("\n}\n")]
+    assert "try_wait" in body and "gave_up" not in body
+    for bar in ("S.done", "S.landed", "S.full"):
+        assert re.search(r"drain_wait\(&%s\b" % bar, text), bar
