@@ -472,3 +472,28 @@ def test_two_threads_at_once():
         check_forward(got[0][0], x, w, counts)
         check_dw(got[0][1], dy, x, counts)
         assert all(torch.equal(got[0][0], y) and torch.equal(got[0][1], dw) for y, dw in got)
+
+
+def test_first_cuda_use_of_a_thread():
+    """A thread that has made no CUDA call yet, nor torch for it."""
+    import threading
+    counts, N, K = [40, 0, 77], 136, 264
+    x, dy, w, c = make(counts, N, K)
+    y, dx, dw = lm.grouped_gemm(x, w, c), lm.grouped_gemm_dx(dy, w, c), lm.grouped_gemm_dw(dy, x, c)
+    for run, out, want in ((lambda o: lm.grouped_gemm(x, w, c, out=o), torch.zeros_like(y), y),
+                           (lambda o: lm.grouped_gemm_dx(dy, w, c, out=o), torch.zeros_like(dx), dx),
+                           (lambda o: lm.grouped_gemm_dw(dy, x, c, out=o), torch.zeros_like(dw), dw)):
+        torch.cuda.synchronize()
+        failed = []
+
+        def work():
+            try:
+                run(out)
+            except Exception as e:
+                failed.append(e)
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not failed and torch.equal(out, want), failed
