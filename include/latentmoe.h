@@ -266,8 +266,11 @@ lmoe_status latentmoe_update_bias(lmoe_handle* h, const int32_t* expert_counts, 
  *  - An output must not overlap an input.
  *  - Stream order holds as for any kernel; a call's launch and set-up may run under
  *    the end of the kernel before it, which it waits for before it touches memory.
- *  - A device wait that runs out of its bound is recorded process-wide and
- *    returned as LMOE_ERR_TIMEOUT by the next of these calls. */
+ *  - A device wait that runs out of its bound (LMOE_ERR_TIMEOUT) leaves its
+ *    launch's outputs undefined; other launches are not affected. It is counted
+ *    process-wide and reported once to every host thread that makes these calls:
+ *    by the thread's next product or gradient, which then launches nothing, or
+ *    by latentmoe_products_status. */
 
 /* y[r, n] = sum_k x[r, k] w[e(r), n, k]: x [n_rows, K] bf16, w [n_groups, N, K]
  * bf16, y [n_rows, N]. */
@@ -307,6 +310,14 @@ lmoe_status latentmoe_quantize_fp8(const void* x, long long ldx, lmoe_dtype x_dt
 lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, const float* ws, const int32_t* counts,
                                int n_groups, int n_rows, int N, int K, void* y, long long ldy, lmoe_dtype y_dtype,
                                int zero_tail, void* stream);
+/* LMOE_ERR_TIMEOUT if a device wait of these calls ran out since this thread's last
+ * report, else LMOE_OK. Launches nothing and does not synchronise: what has run so far
+ * is seen. For programs that replay captured calls, and before results are trusted. */
+lmoe_status latentmoe_products_status(void);
+/* Polls (0 to 2^32 - 1; default 2^24) after which a device wait of calls made from now on
+ * gives up, process-wide; captured calls keep theirs. For tests of the timeout: far fewer
+ * make healthy calls fail. */
+lmoe_status latentmoe_set_products_wait_limit(long long polls);
 
 /* ---- diagnostics --------------------------------------------------------- */
 typedef enum {

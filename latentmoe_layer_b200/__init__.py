@@ -34,7 +34,8 @@ EXPORTS = ["latentmoe_create", "latentmoe_workspace_size", "latentmoe_route", "l
            "latentmoe_selftest_bounded_wait", "latentmoe_set_profile_events", "latentmoe_route_noalloc", "latentmoe_update_bias", "latentmoe_forward_block",
            "latentmoe_quantize_nvfp4", "latentmoe_ep_front", "latentmoe_ep_workspace_size", "latentmoe_ep_experts",
            "latentmoe_ep_back", "latentmoe_workspace_layout", "latentmoe_grouped_gemm", "latentmoe_grouped_gemm_dx",
-           "latentmoe_grouped_gemm_dw", "latentmoe_quantize_fp8", "latentmoe_gemm_fp8"]
+           "latentmoe_grouped_gemm_dw", "latentmoe_quantize_fp8", "latentmoe_gemm_fp8", "latentmoe_products_status",
+           "latentmoe_set_products_wait_limit"]
 
 
 class lmoe_config(ctypes.Structure):
@@ -108,6 +109,8 @@ def load():
     lib.latentmoe_grouped_gemm_dx.argtypes = [vp, ll, vp, vp, i32, i32, i32, i32, vp, ll, i32, i32, vp]
     lib.latentmoe_grouped_gemm_dw.argtypes = [vp, ll, vp, ll, vp, i32, i32, i32, i32, vp, i32, vp]
     lib.latentmoe_quantize_fp8.argtypes = [vp, ll, i32, i32, i32, i32, i32, vp, vp, vp]
+    lib.latentmoe_products_status.argtypes = []
+    lib.latentmoe_set_products_wait_limit.argtypes = [ll]
     lib.latentmoe_gemm_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, ll, i32, i32, vp]
     for f in ("latentmoe_create", "latentmoe_workspace_size", "latentmoe_route", "latentmoe_forward",
               "latentmoe_set_option", "latentmoe_read_stats", "latentmoe_selftest_bounded_wait",
@@ -115,7 +118,8 @@ def load():
               "latentmoe_forward_block", "latentmoe_quantize_nvfp4", "latentmoe_ep_front",
               "latentmoe_ep_workspace_size", "latentmoe_ep_experts", "latentmoe_ep_back",
               "latentmoe_workspace_layout", "latentmoe_grouped_gemm", "latentmoe_grouped_gemm_dx",
-              "latentmoe_grouped_gemm_dw", "latentmoe_quantize_fp8", "latentmoe_gemm_fp8"):
+              "latentmoe_grouped_gemm_dw", "latentmoe_quantize_fp8", "latentmoe_gemm_fp8", "latentmoe_products_status",
+              "latentmoe_set_products_wait_limit"):
         getattr(lib, f).restype = i32
     _lib = lib
     return lib
@@ -213,6 +217,15 @@ def latentmoe_selftest_bounded_wait(h) -> int:
 
 
 # ---------------------------------------------------------------- products without a handle
+def latentmoe_products_status() -> int:
+    """LMOE_ERR_TIMEOUT if a device wait of the products ran out since this thread's last report."""
+    return load().latentmoe_products_status()
+
+
+def latentmoe_set_products_wait_limit(polls: int) -> int:
+    return load().latentmoe_set_products_wait_limit(polls)
+
+
 _PRODUCTS = ("grouped_gemm", "grouped_gemm_dx", "grouped_gemm_dw", "quantize_fp8", "gemm_fp8")
 
 

@@ -45,8 +45,8 @@
 // stored. Features and contraction indices past the matrix are zero-filled by
 // the tensor maps.
 //
-// Every mbarrier wait is bounded; on running out the kernel records
-// LMOE_ERR_TIMEOUT, its cluster waits for its own loads and MMAs, frees TMEM and returns.
+// Every mbarrier wait is bounded; when one runs out the kernel counts it for the host, its
+// cluster waits for its own loads and MMAs, frees TMEM and returns.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -320,7 +320,7 @@ __device__ __forceinline__ void give_up(GgShared& S, const GgParams& P) {
 #pragma unroll 1
     for (uint32_t r = 0; r < n; ++r)
         asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(mapa_shared(&S.gave_up, r)) : "memory");
-    atomicCAS(P.err, 0, 5);
+    atomicAdd(P.err, 1);
 }
 __device__ __forceinline__ bool gave_up(const GgShared& S) {
     int v;

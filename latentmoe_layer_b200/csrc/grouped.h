@@ -23,8 +23,8 @@ struct alignas(64) GgParams {
     int zero_tail;        // 1: rows behind the last group are written as zeros
     int chunk_kb;         // k-blocks per TMEM chunk (8-bit: set by the tile)
     int splits;           // set by launch_grouped: pairs (a cluster of them) that share a tile's contraction
-    int* err;
-    unsigned spin;
+    int* err;             // counts waits that ran out, for the host; never read by a kernel
+    unsigned spin;        // polls after which a wait runs out
 };
 
 // Launches a kernel as a dependent of the one before it in the stream: its launch and

@@ -18,11 +18,13 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-constexpr unsigned kOpsSpin = 1u << 24;
+// Polls after which a device wait gives up.
+std::atomic<unsigned> g_ops_spin{1u << 24};
 
 // What the entry points share, made once per process: the driver's descriptor
-// encoder and a pinned word that a kernel whose bounded wait ran out writes
-// (mapped into every device's address space).
+// encoder and a pinned word in which kernels count the waits that ran out
+// (mapped into every device's address space; the host only reads it, so that
+// no report can be taken from the caller it is meant for).
 struct OpsState {
     EncodeTiledFn encode = nullptr;
     int* herr = nullptr;
@@ -62,10 +64,14 @@ lmoe_status ops_state(const OpsState** out) {
     return LMOE_OK;
 }
 
-// An error that an earlier launch recorded is reported once, by the next call.
+// Waits that ran out since this thread last looked are reported to it once: to every thread,
+// as nothing tells which one's launch it was.
 lmoe_status take_error(const OpsState& st) {
-    const int v = __atomic_exchange_n(st.herr, 0, __ATOMIC_ACQ_REL);
-    return v ? static_cast<lmoe_status>(v) : LMOE_OK;
+    thread_local int seen = 0;
+    const int now = __atomic_load_n(st.herr, __ATOMIC_ACQUIRE);
+    if (now == seen) return LMOE_OK;
+    seen = now;
+    return LMOE_ERR_TIMEOUT;
 }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -144,7 +150,7 @@ GgParams base_params(const OpsState& st, const int32_t* counts, int n_groups, in
     P.out_f32 = out_type == LMOE_FP32;
     P.chunk_kb = chunk_blocks(out_type);
     P.err = st.derr;
-    P.spin = kOpsSpin;
+    P.spin = g_ops_spin.load(std::memory_order_relaxed);
     return P;
 }
 
@@ -257,6 +263,16 @@ lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, 
         return LMOE_ERR_CUDA;
     const int op = n_rows / n_groups > 64 ? GG_FP8_ROWS : GG_FP8;
     return cuda_status(launch_grouped(op, P, static_cast<cudaStream_t>(stream)));
+}
+
+lmoe_status latentmoe_products_status(void) {
+    return g_ops_ready.load(std::memory_order_acquire) ? take_error(g_ops) : LMOE_OK;
+}
+
+lmoe_status latentmoe_set_products_wait_limit(long long polls) {
+    if (polls < 0 || polls > 0xFFFFFFFFLL) return LMOE_ERR_INVALID_ARG;
+    g_ops_spin.store((unsigned)polls, std::memory_order_relaxed);
+    return LMOE_OK;
 }
 
 }  // extern "C"

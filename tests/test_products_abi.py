@@ -105,3 +105,9 @@ def test_binding_refuses_cpu_tensors_and_importing_it_does_not_import_torch():
         lm.no_such_product
     code = "import sys, latentmoe_layer_b200; sys.exit('torch' in sys.modules)"
     assert subprocess.run([sys.executable, "-c", code], cwd=__file__.rsplit("/tests/", 1)[0]).returncode == 0
+
+
+def test_status_and_wait_limit_without_a_gpu(lib):
+    assert lm.latentmoe_products_status() == OK  # nothing has run
+    for polls, status in ((-1, INVALID), (1 << 32, INVALID), (0, OK), ((1 << 32) - 1, OK), (1 << 24, OK)):
+        assert lm.latentmoe_set_products_wait_limit(polls) == status

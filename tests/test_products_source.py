@@ -75,3 +75,10 @@ def test_final_drains_do_not_leave_early():
     assert "try_wait" in body and "gave_up" not in body
     for bar in ("S.done", "S.landed", "S.full"):
         assert re.search(r"drain_wait\(&%s\b" % bar, text), bar
+
+
+def test_the_host_only_reads_the_count_of_timeouts():
+    """Taking the word (an exchange) would give one caller's report to another."""
+    text = code("ops.cu")
+    assert "__atomic_exchange" not in text and "thread_local" in text
+    assert len(re.findall(r"\*st\.herr\s*=", text)) == 1  # its initial zero
