@@ -497,3 +497,28 @@ def test_first_cuda_use_of_a_thread():
         t.join()
         torch.cuda.synchronize()
         assert not failed and torch.equal(out, want), failed
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_long_sums_of_one_sign(dtype):
+    """Contractions of 2^22 like-signed products, where an error of every addition has the same sign.
+
+    Tolerance: at most 4096 products are summed in the tensor core before the sum goes into an fp32
+    register, one of the 1024 sums added there: (4096 + 1024) * 2^-23 of the sum, and rounding the result."""
+    n = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(5)
+    a = (torch.rand(n, 16, generator=g, device="cuda") + 0.5).bfloat16()
+    b = (torch.rand(n, 24, generator=g, device="cuda") + 0.5).bfloat16()
+    ref = torch.zeros(16, 24, dtype=torch.float64, device="cuda")
+    for at in range(0, n, 1 << 18):
+        ref += a[at:at + (1 << 18)].double().t() @ b[at:at + (1 << 18)].double()
+    tol = (HALF_STEP[dtype] + (1 + 2.0 ** -8) * 5120 * 2.0 ** -23) * ref
+    c = torch.tensor([n], dtype=torch.int32, device="cuda")
+    dw = lm.grouped_gemm_dw(a, b, c, out_dtype=dtype)[0]
+    worst = float(((dw.double() - ref).abs() / tol).max())
+    assert worst <= 1.0, worst
+    c = torch.tensor([16], dtype=torch.int32, device="cuda")
+    at, bt = a.t().contiguous(), b.t().contiguous()
+    for got in (lm.grouped_gemm(at, bt[None], c, out_dtype=dtype), lm.grouped_gemm_dx(at, b[None], c, out_dtype=dtype)):
+        worst = float(((got.double() - ref).abs() / tol).max())
+        assert worst <= 1.0, worst
