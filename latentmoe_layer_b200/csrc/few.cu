@@ -198,6 +198,17 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
         }
     };
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    // The lane's sums so far go to its own places in shared memory every 64 steps (4096 products):
+    // the MMA's additions err towards zero, an fp32 result of 2^22 like-signed products came out
+    // 0.3% low. 8-bit sums are drained every step, by the multiply-adds.
+    float(&r0)[9] = red[warp][g], (&r1)[9] = red[warp][g + 8];
+    auto drain = [&](bool first) {
+        r0[c] = first ? acc[0] : r0[c] + acc[0];
+        r0[c + 1] = first ? acc[1] : r0[c + 1] + acc[1];
+        r1[c] = first ? acc[2] : r1[c] + acc[2];
+        r1[c + 1] = first ? acc[3] : r1[c + 1] + acc[3];
+    };
+    constexpr int kDrain = 64;
     fetch(warp, 0);
     if (kRing) fetch(warp + kWarps, 1);
     load(warp);
@@ -234,12 +245,13 @@ __global__ void __launch_bounds__(32 * kWarps, kFewSmWarps / kWarps) k_few(const
             fetch(s + 2 * kWarps, stage);
             stage ^= 1;
         }
+        if (!kF8 && s / kWarps % kDrain == kDrain - 1) {
+            drain(s / kWarps < kDrain);
+            acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+        }
     }
     if (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
-    red[warp][g][2 * t] = acc[0];
-    red[warp][g][2 * t + 1] = acc[1];
-    red[warp][g + 8][2 * t] = acc[2];
-    red[warp][g + 8][2 * t + 1] = acc[3];
+    drain(kF8 || steps <= warp + kWarps * (kDrain - 1));
     __syncthreads();
     static_assert(32 * kWarps >= kFewFeats * 8, "a thread per output");
     if (threadIdx.x < kFewFeats * 8) {

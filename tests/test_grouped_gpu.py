@@ -522,3 +522,26 @@ def test_long_sums_of_one_sign(dtype):
     for got in (lm.grouped_gemm(at, bt[None], c, out_dtype=dtype), lm.grouped_gemm_dx(at, b[None], c, out_dtype=dtype)):
         worst = float(((got.double() - ref).abs() / tol).max())
         assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_long_sums_of_one_sign_few_rows(dtype):
+    """The same for the kernel of up to eight rows: 4096 products of a warp, then its sum in shared memory
+    (2^22 / 4096 / warps of them), then the warps'; fewer than 1024 in all."""
+    n = 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x = (torch.rand(5, n, generator=g, device="cuda") + 0.5).bfloat16()
+    w = (torch.rand(24, n, generator=g, device="cuda") + 0.5).bfloat16()
+    c = torch.tensor([5], dtype=torch.int32, device="cuda")
+    ref = sum(x[:, at:at + (1 << 18)].double() @ w[:, at:at + (1 << 18)].double().t() for at in range(0, n, 1 << 18))
+    tol = (HALF_STEP[dtype] + (1 + 2.0 ** -8) * 5120 * 2.0 ** -23) * ref
+    worst = float(((lm.grouped_gemm(x, w[None], c, out_dtype=dtype).double() - ref).abs() / tol).max())
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("N", [24, 8200, 16008])  # eight warps, four with the ring, four without
+@pytest.mark.parametrize("K", [4096, 32768 + 72])
+def test_few_rows_past_a_drain(N, K):
+    counts = [3, 0, 2]
+    x, _, w, c = make(counts, N, K, rows=7)
+    check_forward(lm.grouped_gemm(x, w, c, out_dtype=torch.float32), x, w, counts)
