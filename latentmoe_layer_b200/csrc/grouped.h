@@ -45,8 +45,7 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, int 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kernel, args...);  // this launch's error, no earlier call's
 }
 
 // GG_FWD (f8 = false) and GG_FP8 for up to kFewRows rows, where the kernel that splits a matrix over

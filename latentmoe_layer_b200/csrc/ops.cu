@@ -34,6 +34,12 @@ std::mutex g_ops_mu;
 OpsState g_ops;
 std::atomic<bool> g_ops_ready{false};
 
+// An error that is returned is not left behind for a later call's cudaGetLastError.
+lmoe_status failed() {
+    (void)cudaGetLastError();
+    return LMOE_ERR_CUDA;
+}
+
 lmoe_status ops_state(const OpsState** out) {
     if (!g_ops_ready.load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(g_ops_mu);
@@ -41,7 +47,7 @@ lmoe_status ops_state(const OpsState** out) {
             OpsState st;
             // the first call may come while a stream is being captured: the allocation is not part of the graph
             cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-            if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return LMOE_ERR_CUDA;
+            if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return failed();
             void* fn = nullptr;
             cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
             bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
@@ -52,7 +58,7 @@ lmoe_status ops_state(const OpsState** out) {
             if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) ok = false;
             if (!ok) {
                 if (st.herr) cudaFreeHost(st.herr);
-                return LMOE_ERR_CUDA;
+                return failed();
             }
             *st.herr = 0;
             st.encode = reinterpret_cast<EncodeTiledFn>(fn);
@@ -75,7 +81,7 @@ lmoe_status take_error(const OpsState& st) {
 }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline lmoe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LMOE_OK : LMOE_ERR_CUDA; }
+inline lmoe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? LMOE_OK : failed(); }
 
 // [mats, rows, cols] with a row pitch, boxes of 128 bytes x box_rows, 128-byte
 // swizzle; indices past the end are filled with zeros.
@@ -179,7 +185,7 @@ lmoe_status run_rows(bool dx, const void* a, long long lda, const void* w, const
         return cuda_status(launch_few(false, w, a, lda * 2, P, static_cast<cudaStream_t>(stream)));
     if (!encode(*st, &P.a_map, w, true, n_groups, N, K, K, dx ? 64 : 128) ||
         !encode_rows(*st, P, a, true, n_rows, in_cols, lda))
-        return LMOE_ERR_CUDA;
+        return failed();
     return cuda_status(launch_grouped(dx ? GG_DX : GG_FWD, P, static_cast<cudaStream_t>(stream)));
 }
 
@@ -219,7 +225,7 @@ lmoe_status latentmoe_grouped_gemm_dw(const void* dy, long long lddy, const void
     P.feat = K;
     P.cols = N;
     if (!encode(*st, &P.a_map, x, true, 1, n_rows, K, ldx, 64) || !encode(*st, &P.b_map[0], dy, true, 1, n_rows, N, lddy, 64))
-        return LMOE_ERR_CUDA;
+        return failed();
     return cuda_status(launch_grouped(GG_DW, P, static_cast<cudaStream_t>(stream)));
 }
 
@@ -262,7 +268,7 @@ lmoe_status latentmoe_gemm_fp8(const void* xq, const float* xs, const void* wq, 
         return cuda_status(launch_few(true, wq, xq, K, P, static_cast<cudaStream_t>(stream)));
     if (!encode(*st, &P.a_map, wq, false, n_groups, N, K, K, 128) ||
         !encode_rows(*st, P, xq, false, n_rows, K, K))
-        return LMOE_ERR_CUDA;
+        return failed();
     const int op = n_rows / n_groups > 64 ? GG_FP8_ROWS : GG_FP8;
     return cuda_status(launch_grouped(op, P, static_cast<cudaStream_t>(stream)));
 }
