@@ -5,8 +5,10 @@ their gradients, the 8-bit quantiser and the block-scaled 8-bit product
 Argument marshalling only, like the rest of the binding: every function checks
 its tensors (ValueError), launches on the current stream of the tensors' device
 and raises ``LmoeError`` on a status from the library. Nothing synchronises, no
-workspace is kept, and the calls can be captured into a CUDA graph. None of them
-records an autograd graph: the gradients are calls of their own.
+workspace is kept, and the calls can be captured into a CUDA graph.
+
+None of them records an autograd graph: the gradients are calls of their own. A write
+to ``out`` is known to autograd (its version counts up).
 
 The smallest calls take longer to issue than to run (8 us against 4), so the
 checks touch each attribute once, in one expression, and the text of a refusal
@@ -15,6 +17,7 @@ is put together afterwards.
 from __future__ import annotations
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import LMOE_BF16, LMOE_FP32, LMOE_OK, LmoeError, load
 
@@ -59,6 +62,12 @@ def _out(where, out, dtype, x, shape):
     if not out.is_contiguous():
         raise ValueError("%s: out must be contiguous (strides %s)" % (where, out.stride()))
     return out, shape[-1], code
+
+
+def _written(out):
+    """Autograd hears of a write that it did not make."""
+    if not out.is_inference():
+        increment_version(out)
 
 
 def _launch(fn, index, *args):
@@ -107,6 +116,8 @@ def grouped_gemm(x, w, counts, out=None, out_dtype=None, zero_tail=False):
     ldx = K if x.is_contiguous() else _pitch(x, rows, K, "x", "grouped_gemm")
     _launch("latentmoe_grouped_gemm", index, x.data_ptr(), ldx, w.data_ptr(), counts.data_ptr(), E, rows, N, K,
             y.data_ptr(), ldy, code, zero_tail)
+    if out is not None:
+        _written(out)
     return y
 
 
@@ -128,6 +139,8 @@ def grouped_gemm_dx(dy, w, counts, out=None, out_dtype=None, zero_tail=False):
     lddy = N if dy.is_contiguous() else _pitch(dy, rows, N, "dy", "grouped_gemm_dx")
     _launch("latentmoe_grouped_gemm_dx", index, dy.data_ptr(), lddy, w.data_ptr(), counts.data_ptr(), E, rows, N, K,
             dx.data_ptr(), lddx, code, zero_tail)
+    if out is not None:
+        _written(out)
     return dx
 
 
@@ -151,6 +164,8 @@ def grouped_gemm_dw(dy, x, counts, out=None, out_dtype=None):
     ldx = K if x.is_contiguous() else _pitch(x, rows, K, "x", "grouped_gemm_dw")
     _launch("latentmoe_grouped_gemm_dw", index, dy.data_ptr(), lddy, x.data_ptr(), ldx, counts.data_ptr(), E, rows,
             N, K, dw.data_ptr(), code)
+    if out is not None:
+        _written(out)
     return dw
 
 
@@ -210,4 +225,6 @@ def gemm_fp8(xq, xs, wq, ws, counts=None, out=None, out_dtype=None, zero_tail=Fa
     y, ldy, code = _out("gemm_fp8", out, out_dtype, xq, (rows, N))
     _launch("latentmoe_gemm_fp8", index, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), ptr, E, rows, N, K,
             y.data_ptr(), ldy, code, zero_tail)
+    if out is not None:
+        _written(out)
     return y
