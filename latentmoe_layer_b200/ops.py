@@ -7,8 +7,9 @@ its tensors (ValueError), launches on the current stream of the tensors' device
 and raises ``LmoeError`` on a status from the library. Nothing synchronises, no
 workspace is kept, and the calls can be captured into a CUDA graph.
 
-None of them records an autograd graph: the gradients are calls of their own. A write
-to ``out`` is known to autograd (its version counts up).
+``grouped_gemm`` is differentiable once, in x and w. The others record no autograd
+graph: the gradients are there to be called, and 8-bit codes have none. A write to
+``out`` is known to autograd (its version counts up).
 
 The smallest calls take longer to issue than to run (8 us against 4), so the
 checks touch each attribute once, in one expression, and the text of a refusal
@@ -17,6 +18,7 @@ is put together afterwards.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
 from . import LMOE_BF16, LMOE_FP32, LMOE_OK, LmoeError, load
@@ -100,7 +102,14 @@ def grouped_gemm(x, w, counts, out=None, out_dtype=None, zero_tail=False):
     """y[r] = x[r] W[e(r)]^T: x [rows, K] bf16 in expert order, w [E, N, K] bf16,
     counts [E] int32 rows per expert (on the device). Returns y [rows, N] in
     out_dtype (bfloat16 unless given, or out's). Rows behind the last expert's
-    keep what they held; zero_tail writes zeros there."""
+    keep what they held; zero_tail writes zeros there.
+
+    Where x or w requires a gradient it is recorded (not with out=, which is refused
+    then): backward gives dx, zeros behind the last expert, and dw, both bfloat16."""
+    if (x.requires_grad or w.requires_grad) and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("grouped_gemm: out= records no gradient, and x or w requires one (use torch.no_grad())")
+        return _GroupedGemm.apply(x, w, counts, out_dtype, zero_tail)
     index = x.get_device()
     if (index < 0 or x.dtype is not _BF16 or x.dim() != 2 or w.dtype is not _BF16 or w.dim() != 3 or counts.dtype is not _I32
             or counts.dim() != 1 or w.get_device() != index or counts.get_device() != index or not w.is_contiguous()
@@ -119,6 +128,26 @@ def grouped_gemm(x, w, counts, out=None, out_dtype=None, zero_tail=False):
     if out is not None:
         _written(out)
     return y
+
+
+class _GroupedGemm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, counts, out_dtype, zero_tail):
+        ctx.save_for_backward(x, w, counts)
+        return grouped_gemm(x, w, counts, out_dtype=out_dtype, zero_tail=zero_tail)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, w, counts = ctx.saved_tensors
+        # of any strides (sum() hands down strides of 0), and fp32 for an fp32 output: the products
+        # read bf16, so that gradient is rounded once, as bf16 activations' are
+        dy = dy.to(_BF16).contiguous()
+        if dy.data_ptr() % 16:
+            dy = dy.clone()
+        dx = grouped_gemm_dx(dy, w, counts, zero_tail=True) if ctx.needs_input_grad[0] else None
+        dw = grouped_gemm_dw(dy, x, counts) if ctx.needs_input_grad[1] else None
+        return dx, dw, None, None, None
 
 
 def grouped_gemm_dx(dy, w, counts, out=None, out_dtype=None, zero_tail=False):
