@@ -36,6 +36,8 @@
 //                  on the 128-row side so no tensor-core work is padding).
 // Every mbarrier wait is bounded; on running out the kernel records
 // LMOE_ERR_TIMEOUT, drains its own TMA loads and MMAs, frees TMEM and returns.
+#include <atomic>
+
 #include "gemm_common.cuh"
 
 namespace lmoe {
@@ -558,18 +560,18 @@ cudaError_t launch_impl(const TcParams& P, int grid, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-int g_num_sms = 0;
+constexpr int kMaxSmDevices = 64;
+std::atomic<int> g_num_sms[kMaxSmDevices];  // by device; 0: not asked yet
 
 }  // namespace
 
 int tc_num_sms() {
-    if (g_num_sms == 0) {
-        int dev = 0, n = 0;
-        cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        g_num_sms = n > 0 ? n : 148;
-    }
-    return g_num_sms;
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) dev = 0;
+    if (dev < kMaxSmDevices && (n = g_num_sms[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    if (dev < kMaxSmDevices) g_num_sms[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 // Dense tile counts (host side) and a grid no larger than the work.

@@ -82,3 +82,11 @@ def test_the_host_only_reads_the_count_of_timeouts():
     text = code("ops.cu")
     assert "__atomic_exchange" not in text and "thread_local" in text
     assert len(re.findall(r"\*st\.herr\s*=", text)) == 1  # its initial zero
+
+
+def test_the_sm_count_is_kept_by_device():
+    """Grids and the few-row kernel's share of an SM follow the current device, and two threads may ask at once."""
+    text = code("gemm_tc.cu")
+    body = text[text.index("int tc_num_sms()"):]
+    body = body[:body.index("\n}\n")]
+    assert re.search(r"std::atomic<int>\s+g_num_sms\[", text) and "cudaGetDevice" in body and "[dev]" in body
