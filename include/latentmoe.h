@@ -261,8 +261,11 @@ lmoe_status latentmoe_update_bias(lmoe_handle* h, const int32_t* expert_counts, 
  *    N a multiple of 8, K of 8 (fp8: 16), both at most 2^22, n_rows at most 2^30
  *    (0 is allowed), at most 2^38 elements per operand (else
  *    LMOE_ERR_UNSUPPORTED).
- *  - Outputs are bf16 (one rounding from fp32, nearest-even) or fp32. NaN and
- *    infinities stay in the rows (for dw: in the group) that they belong to.
+ *  - Sums are fp32 throughout; outputs are bf16 (one rounding, nearest-even) or
+ *    fp32. The tensor core adds up to 512 products (bf16 outputs and calls of up to
+ *    8 rows: 4096; fp8: a block of 128) before the sum goes into an fp32 register;
+ *    its own additions err towards zero, by about 1e-7 of the sum per 16 products of
+ *    one sign. NaN and infinities stay in the rows (for dw: in the group) that they belong to.
  *  - An output must not overlap an input.
  *  - Stream order holds as for any kernel; a call's launch and set-up may run under
  *    the end of the kernel before it, which it waits for before it touches memory.

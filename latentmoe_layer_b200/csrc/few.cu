@@ -45,7 +45,7 @@ struct FewParams {
     const float* x_scale;   // 8-bit: [n_rows, ceil(cdim / 128)]
     void* out;
     long long ldo;
-    int n_groups, n_rows, slots, feat, cdim, out_f32, zero_tail;
+    int n_groups, n_rows, slots, feat, cdim, out_f32;
 };
 
 template <bool kF8>
@@ -309,7 +309,6 @@ cudaError_t launch_few(bool f8, const void* w, const void* x, long long ldx_byte
     P.feat = G.feat;
     P.cdim = G.cdim;
     P.out_f32 = G.out_f32;
-    P.zero_tail = G.zero_tail;
     const dim3 grid((G.feat + kFewFeats - 1) / kFewFeats, P.slots + (G.counts && G.zero_tail ? 1 : 0));
     // Eight warps per CTA where all those CTAs fit at once: its contraction is shared by more (1024 x 8192, one
     // row: 5.8 us; four warps 8.7, the ring 7.2). Beyond that four, as twice as many CTAs are resident: through

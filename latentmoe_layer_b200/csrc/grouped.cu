@@ -10,12 +10,15 @@
 //   GG_DX   dx[r, k] = sum_n dy[r, n] W[e][n, k]      A = W^T (MN-major) B = dy (K-major)
 //   GG_DW   dW[e][n, k] = sum_{r in e} dy[r, n] x[r, k]  A = x^T, B = dy^T (both MN-major)
 //   GG_FP8  y[r, n] = sum_b sx[r, b] sw[e][n/128, b] sum_{k in block b} xq[r, k] wq[e][n, k]
+//   GG_FP8_ROWS  the same with the rows on M and the features on N (epilogue_rows)
 //
-// Why the features are on M. A batch's groups are uneven, and rows on M would
+// Why the features are on M elsewhere. A batch's groups are uneven, and rows on M would
 // be padded to 256 per group; the MMA's N takes any multiple of 32, so the
 // ragged end of a group costs its own rows only, and a decode batch (a few rows
-// per expert) streams each weight tile once with N = 32. It also makes lanes
-// consecutive in the output's fast axis, so stores need no transposition.
+// per expert) streams each weight tile once with N = 32. The price is a
+// transposition of the output, through 2 KB of shared memory per warp (store_rows).
+// GG_FP8_ROWS takes large groups, where rounding up to 256 rows costs less than
+// one scale per lane gains in the drain.
 //
 // Why pairs. 128 x 256 tiles on single SMs read 48 KB of operands per 64-deep
 // k-block, 96 bytes per SM and cycle at the tensor peak; a pair's 256 x 256 tile
@@ -23,8 +26,8 @@
 //
 // Structure of one CTA of a pair (one pair per two SMs, persistent over tiles):
 //   warp 0       TMA producer (own 128 features of A, own half of B's rows)
-//   warp 1       TMEM owner; in the leader CTA, lane 0 issues the MMAs
-//   warps 2, 3   GG_FP8: the products sx * sw of the next four k-blocks, into
+//   warp 1       TMEM owner; in the leader CTA, an elected lane issues the MMAs
+//   warps 2, 3   8-bit: the products sx * sw of the next four k-blocks, into
 //                shared memory; GG_DW: zeros behind a group's last row
 //   warps 4-11   epilogue: drain TMEM chunks into fp32 registers, store
 // Tiles are found from prefix sums of the counts that every CTA builds in
@@ -32,7 +35,7 @@
 //
 // Accumulation: TMEM holds a chunk of the contraction (two buffers of 256
 // columns), the epilogue adds chunks into fp32 registers while the next one
-// runs. GG_FP8 drains every 128-deep block, where its two scales are applied
+// runs. The 8-bit forms drain every 128-deep block, where its two scales are applied
 // as one fused multiply-add per element (their product is rounded to fp32
 // once). fp32 outputs drain every 512, which keeps the tensor core's
 // accumulation error near that of fp32 additions; bf16 outputs drain every 4096,
@@ -45,8 +48,8 @@
 // stored. Features and contraction indices past the matrix are zero-filled by
 // the tensor maps.
 //
-// Every mbarrier wait is bounded; when one runs out the kernel counts it for the host, its
-// cluster waits for its own loads and MMAs, frees TMEM and returns.
+// Every mbarrier wait is bounded (2^24 polls of 4.5 us: 75 s); when one runs out the kernel
+// counts it for the host, its cluster waits for its own loads and MMAs, frees TMEM and returns.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -402,8 +405,8 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* r) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// Waits for the loads so far. The uses of their registers (below) are volatile too, which
-// keeps the compiler from moving them ahead of it.
+// Waits for the loads so far. Every use of their registers (below) is volatile asm, which
+// keeps its order after this one; other code must not touch them.
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // acc += (lo, hi) and acc += (lo, hi) * s for registers that a load has written.
 __device__ __forceinline__ void add_loaded(uint64_t& acc, uint32_t lo, uint32_t hi) {
