@@ -70,6 +70,7 @@ constexpr int kGgEpiWarps = 8;
 constexpr int kGgRaster = 8;          // N-side tiles per raster block (shared weight reads in L2)
 constexpr int kScaleBatch = 4;        // k-blocks per batch of scale products
 // Registers per thread: 128 x producers' + 256 x epilogue's must not exceed 384 x kLaunchRegs.
+// (8-bit: with 56 the scale warps spill, which cost the dense prompt 10%.)
 constexpr int kLaunchRegs = 168;
 template <int OP>
 struct GgRegs {
